@@ -26,37 +26,37 @@ MIN_SCALE = 2.0 ** -126
 def listed():
     return [
         # one decoded token of the DeepSeek-V2-Lite-shaped layer: latency
-        dict(name="norm, one token", op="norm", T=1, H=2048, dtype="bf16", residual=True, group=0),
+        dict(name="norm one token", op="norm", T=1, H=2048, dtype="bf16", residual=True, group=0),
         # an odd width and a ragged batch in fp32, no residual yet (first layer)
-        dict(name="norm, odd width fp32", op="norm", T=129, H=1413, dtype="f32", residual=False,
+        dict(name="norm odd width fp32", op="norm", T=129, H=1413, dtype="f32", residual=False,
              group=0),
         # the 8192-token prefill layer, rows also sent on in 8 bits
-        dict(name="norm, prefill and 8 bits", op="norm", T=8192, H=4096, dtype="bf16",
+        dict(name="norm prefill and 8 bits", op="norm", T=8192, H=4096, dtype="bf16",
              residual=True, group=128),
         # a short training batch of the DeepSeek-V2-Lite-shaped layer
-        dict(name="norm gradient, 300 tokens", op="norm_backward", T=300, H=2048, dtype="f16",
+        dict(name="norm gradient 300 tokens", op="norm_backward", T=300, H=2048, dtype="f16",
              residual=True),
         # the prefill layer's batch as a training batch
-        dict(name="norm gradient, 8192 tokens", op="norm_backward", T=8192, H=4096, dtype="bf16",
+        dict(name="norm gradient 8192 tokens", op="norm_backward", T=8192, H=4096, dtype="bf16",
              residual=True),
         # the largest small batch of the layer, 64 experts top-6: latency
-        dict(name="balance, 64 tokens", op="balance", T=64, E=64, k=6, mode="softmax", seqs=1,
+        dict(name="balance 64 tokens", op="balance", T=64, E=64, k=6, mode="softmax", seqs=1,
              mask=False),
         # the prefill layer's routing, one sequence
-        dict(name="balance, 8192 tokens", op="balance", T=8192, E=256, k=8, mode="softmax", seqs=1,
+        dict(name="balance 8192 tokens", op="balance", T=8192, E=256, k=8, mode="softmax", seqs=1,
              mask=False),
         # a packed training batch of ragged, partly padded sequences, the
         # sigmoid-routed layer's 256 experts top-10
-        dict(name="balance, packed sequences", op="balance", T=131072, E=256, k=10, mode="sigmoid",
+        dict(name="balance packed sequences", op="balance", T=131072, E=256, k=10, mode="sigmoid",
              seqs=37, mask=True),
         # a short batch of the DeepSeek-V2-Lite-shaped router
-        dict(name="router gradient, 129 tokens", op="route_backward", T=129, H=2048, E=64, k=6,
+        dict(name="router gradient 129 tokens", op="route_backward", T=129, H=2048, E=64, k=6,
              mode="softmax"),
         # few experts, sigmoid routing
-        dict(name="router gradient, 32 experts", op="route_backward", T=2048, H=4096, E=32, k=8,
+        dict(name="router gradient 32 experts", op="route_backward", T=2048, H=4096, E=32, k=8,
              mode="sigmoid"),
         # the prefill layer's router and batch
-        dict(name="router gradient, 8192 tokens", op="route_backward", T=8192, H=4096, E=256, k=8,
+        dict(name="router gradient 8192 tokens", op="route_backward", T=8192, H=4096, E=256, k=8,
              mode="softmax"),
     ]
 
