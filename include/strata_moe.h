@@ -376,6 +376,59 @@ strata_status strata_arena_prefill(strata_arena *a, const void *x_bf16, int n_to
 strata_status strata_moe_forward_noalloc(strata_moe *h, const void *x_bf16, int n_tokens,
                                          void *out_bf16, strata_stream_t stream);
 
+/* ---- The norm in front of the layer.  The pages describe no such call; a
+ * user of the layer needs it between the residual stream and the router.
+ *
+ * Element types of the rows (STRATA_DTYPE_*).  Weights are fp32, as the
+ * router's are. */
+enum { STRATA_DTYPE_BF16 = 0, STRATA_DTYPE_F16 = 1, STRATA_DTYPE_F32 = 2 };
+
+/* RMS norm of n_tokens rows of `hidden` elements with the residual's addition:
+ *     s = x + residual,   y = s / sqrt(mean(s^2) + eps) * weight,
+ * in fp32 (the mean and y take s before its rounding), each output rounded
+ * once to nearest even.  x, residual, residual_out, out: device rows of type
+ * `dtype`, row t starting at element t * stride (strides in elements, >= hidden;
+ * ignored for one row).  residual may be NULL (s = x); residual_out (receives
+ * s) may be NULL; out (receives y) may be NULL if out_q8 is given.  weight:
+ * device fp32 [hidden].  residual_out may be x or residual, and out any of the
+ * three inputs, in the same place (same address and stride); residual_out and
+ * out must not overlap.
+ * out_q8 (or NULL): device e4m3 [n_tokens][hidden], contiguous, with one fp32
+ * scale per `group` consecutive columns of a row, scales [n_tokens]
+ * [ceil(hidden / group)]: scale = max(largest |y| of the group / 448, 2^-126),
+ * q = e4m3(y / scale) (nearest even); y is the fp32 value, not the rounded
+ * out.  group: 32, 64, 128, or >= hidden for one scale a row.  A group that
+ * holds a NaN gets a NaN scale.
+ * 16-byte aligned rows of a multiple of 8 elements are fastest; any element
+ * alignment works.  Runs on the current device, asynchronous on `stream`; no
+ * workspace.  Errors: INVALID_ARG, UNSUPPORTED (hidden > 16384), CUDA. */
+strata_status strata_rmsnorm(int dtype, const void *x, long long x_stride, const void *residual,
+                             long long residual_stride, const float *weight, float eps,
+                             int n_tokens, int hidden, void *residual_out,
+                             long long residual_out_stride, void *out, long long out_stride,
+                             void *out_q8, float *scales, int group, strata_stream_t stream);
+
+/* Gradient of strata_rmsnorm at the saved sum h (its residual_out, or x where
+ * there was no residual).  dout: gradient of out; dsum (or NULL): gradient that
+ * reaches residual_out directly.  With i = 1 / sqrt(mean(h^2) + eps) and
+ * gy = dout * weight:
+ *     dx = i * gy - h * i^3 * mean(gy * h) + dsum
+ *     dweight = sum over tokens of dout * h * i
+ * dx (type `dtype`) is the gradient of both x and residual; it may be h, dout
+ * or dsum in the same place.  dweight: device fp32 [hidden], or NULL.  The sums
+ * are taken in a fixed order: the same inputs give the same bits.
+ * workspace: device memory of strata_rmsnorm_backward_workspace bytes, 16-byte
+ * aligned, written before it is read; NULL if dweight is.  Calls that may
+ * overlap on the GPU need a workspace each.  n_tokens == 0 zeroes dweight.
+ * Errors: INVALID_ARG, UNSUPPORTED (hidden > 16384), CUDA. */
+size_t strata_rmsnorm_backward_workspace(int n_tokens, int hidden);
+strata_status strata_rmsnorm_backward(int dtype, const void *h, long long h_stride,
+                                      const float *weight, float eps, const void *dout,
+                                      long long dout_stride, const void *dsum,
+                                      long long dsum_stride, int n_tokens, int hidden, void *dx,
+                                      long long dx_stride, float *dweight, void *workspace,
+                                      size_t workspace_bytes, strata_stream_t stream);
+
 /* Human-readable name of a status. */
 const char *strata_status_str(strata_status s);
 

@@ -56,6 +56,7 @@ def load_library():
                                "quantized_routed_expert_04_b200.build)")
         lib = ctypes.CDLL(LIB_PATH)
         P, I, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+        L, F = ctypes.c_longlong, ctypes.c_float
         sig = {
             "strata_moe_create": (I, [I, I, I, I, I, I, ctypes.POINTER(P)]),
             "strata_moe_destroy": (None, [P]),
@@ -77,6 +78,9 @@ def load_library():
             "strata_moe_profile": (I, [P, I]),
             "strata_moe_set_wait_limit": (I, [P, ctypes.c_ulonglong]),
             "strata_moe_profile_read": (I, [P, I, P, P]),
+            "strata_rmsnorm": (I, [I, P, L, P, L, P, F, I, I, P, L, P, L, P, P, I, P]),
+            "strata_rmsnorm_backward_workspace": (Z, [I, I]),
+            "strata_rmsnorm_backward": (I, [I, P, L, P, F, P, L, P, L, I, I, P, L, P, P, Z, P]),
             "strata_status_str": (ctypes.c_char_p, [I]),
             "strata_arena_create": (I, [P, P, P, ctypes.POINTER(P)]),
             "strata_arena_destroy": (None, [P]),
@@ -224,6 +228,102 @@ def strata_moe_profile_read(h):
     ms = (ctypes.c_double * n)()
     _check(_load().strata_moe_profile_read(h, n, launches, ms), "strata_moe_profile_read")
     return {PHASES[i]: (launches[i], ms[i]) for i in range(n)}
+
+
+DTYPE_BF16, DTYPE_F16, DTYPE_F32 = 0, 1, 2
+_dtypes = None   # torch dtype -> code, filled on first use (torch is imported lazily)
+
+
+def _dtype(t):
+    global _dtypes
+    if _dtypes is None:
+        import torch
+        _dtypes = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}
+    return _dtypes.get(t.dtype, -1)
+
+
+def _refuse(where):
+    raise StrataError(Status.INVALID_ARG, where)
+
+
+def _rows(t, like, where):
+    """(address, row stride) of a 2-D row operand that goes with `like`, or (None, 0)."""
+    if t is None:
+        return None, 0
+    if (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device
+            or (t.stride(1) != 1 and t.shape[1] > 1)):
+        _refuse(where)
+    return t.data_ptr(), t.stride(0)
+
+
+def _flat(t, like, n, itemsize, where):
+    """Address of a contiguous operand of n elements of itemsize bytes, or None."""
+    if t is None:
+        return None
+    if (t.numel() != n or t.element_size() != itemsize or t.device != like.device
+            or not t.is_contiguous()):
+        _refuse(where)
+    return t.data_ptr()
+
+
+def _on_current(t, where):
+    """A kernel runs on the current device: its operands have to be there."""
+    import torch
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        _refuse(where)
+
+
+def strata_rmsnorm(x, residual, weight, eps, residual_out=None, out=None, out_q8=None, scales=None,
+                   group=0, stream=None):
+    """Rows are torch tensors [tokens][hidden] with unit column stride."""
+    w = "strata_rmsnorm"
+    code = _dtype(x)
+    if x.dim() != 2:
+        _refuse(w)
+    T, H = x.shape
+    xa, ldx = _rows(x, x, w)
+    ra, ldr = _rows(residual, x, w)
+    roa, ldro = _rows(residual_out, x, w)
+    oa, ldo = _rows(out, x, w)
+    sa = qa = None
+    if out_q8 is not None:
+        if group <= 0 or scales is None:
+            _refuse(w)
+        qa = _flat(out_q8, x, T * H, 1, w)
+        sa = _flat(scales, x, T * -(-H // group), 4, w)
+    _on_current(x, w)
+    _check(_load().strata_rmsnorm(code, xa, ldx, ra, ldr, _flat(weight, x, H, 4, w), eps, T, H, roa,
+                                  ldro, oa, ldo, qa, sa, group, _stream(stream)), w)
+
+
+def strata_rmsnorm_backward_workspace(n_tokens, hidden):
+    return int(_load().strata_rmsnorm_backward_workspace(n_tokens, hidden))
+
+
+def strata_rmsnorm_backward(h, weight, eps, dout, dsum, dx, dweight=None, workspace=None,
+                            stream=None):
+    w = "strata_rmsnorm_backward"
+    code = _dtype(h)
+    if h.dim() != 2:
+        _refuse(w)
+    T, H = h.shape
+    ha, ldh = _rows(h, h, w)
+    da, ldd = _rows(dout, h, w)
+    sa, lds = _rows(dsum, h, w)
+    xa, ldx = _rows(dx, h, w)
+    ws, nws = _workspace(workspace, h, w)
+    _on_current(h, w)
+    _check(_load().strata_rmsnorm_backward(code, ha, ldh, _flat(weight, h, H, 4, w), eps, da, ldd,
+                                           sa, lds, T, H, xa, ldx, _flat(dweight, h, H, 4, w), ws,
+                                           nws, _stream(stream)), w)
+
+
+def _workspace(t, like, where):
+    if t is None:
+        return None, 0
+    if t.device != like.device or not t.is_contiguous():
+        _refuse(where)
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def strata_status_str(st):

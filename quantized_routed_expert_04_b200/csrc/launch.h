@@ -1,0 +1,37 @@
+// Host-side launch helpers shared by the operators around the expert layer.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <utility>
+
+#include "strata_moe.h"
+
+namespace strata {
+
+inline strata_status status_of(cudaError_t e) {
+  if (e == cudaSuccess) return STRATA_OK;
+  if (e == cudaErrorMemoryAllocation) return STRATA_ERR_OOM;
+  return STRATA_ERR_CUDA;
+}
+
+// Launch with programmatic dependent launch: the grid may be set up while the
+// kernel before it on the stream drains (every kernel launched this way
+// begins with griddepcontrol.wait, before any access to global memory).
+template <typename... Exp, typename... Act>
+cudaError_t launch_pdl(void (*kern)(Exp...), dim3 grid, dim3 block, size_t smem,
+                       cudaStream_t stream, Act &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Act>(args)...);
+}
+
+}  // namespace strata

@@ -1,0 +1,597 @@
+// RMS norm with the residual's addition, its output in 16 or 32 bits and/or
+// in e4m3 with scales, and its gradient.
+//
+// Forward, per row: s = x + r, y = s * rsqrt(mean(s^2) + eps) * g.  Gradient,
+// with i = rsqrt(mean(h^2) + eps) of the saved sum h and gy = dy * g:
+//   dx = i gy - h i^3 mean(gy h) + ds,   dg = sum over rows of dy h i.
+// Everything between the loads and the stores is fp32: s (not its rounding)
+// is what is squared and normalised, and each output is rounded once.
+//
+// Both are bound by HBM: a row is read once, kept in registers through its
+// reduction, and written once.  Element mapping: with 16-byte aligned rows
+// (kVec) a thread holds groups of 8 consecutive elements, one 16-byte access
+// each (two for fp32); otherwise the block's threads take consecutive
+// elements one by one, which keeps every access of a warp contiguous.
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace strata {
+
+namespace {
+
+constexpr int kNormMaxH = 16384;
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_f32(float v) { return v; }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ float from_f32(float v) { return v; }
+
+// Eight elements as they are stored.
+template <typename T>
+struct alignas(16) Vec8 {
+  T v[8];
+};
+
+// Plain loads and stores (never the read-only path: an output may be the same
+// buffer as an input).
+template <typename T>
+__device__ __forceinline__ Vec8<T> load8(const T *p) {
+  Vec8<T> r;
+  uint4 *d = reinterpret_cast<uint4 *>(&r);
+  const uint4 *s = reinterpret_cast<const uint4 *>(p);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(Vec8<T>) / 16; ++i) d[i] = s[i];
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void store8(T *p, const Vec8<T> &r) {
+  const uint4 *s = reinterpret_cast<const uint4 *>(&r);
+  uint4 *d = reinterpret_cast<uint4 *>(p);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(Vec8<T>) / 16; ++i) d[i] = s[i];
+}
+
+// max that keeps a NaN (a group with a NaN gets a NaN scale, so that it reads
+// back as NaN)
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Four floats -> four e4m3 bytes (nearest even, saturating at 448, NaN kept).
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// Step of a group whose largest magnitude is amax: amax / 448, but never
+// below the smallest normal fp32 (an all-zero group divides by it safely).
+__device__ __forceinline__ float e4m3_step(float amax) {
+  return max_nan(__fdiv_rn(amax, 448.0f), 1.17549435e-38f);
+}
+
+struct SumOp {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+struct MaxOp {
+  __device__ __forceinline__ float operator()(float a, float b) const { return max_nan(a, b); }
+};
+
+// Reduction over the kTpr threads of a row, the result in every one of them.
+// slots: kTpr / 32 floats of shared memory that no other reduction in flight
+// uses.
+template <int kTpr, typename Op>
+__device__ __forceinline__ float row_reduce(float v, Op op, float *slots, int tid) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if (kTpr > 32) {
+    constexpr int kWarps = kTpr / 32;
+    if ((tid & 31) == 0) slots[tid >> 5] = v;
+    __syncthreads();
+    v = slots[tid & (kWarps - 1)];
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+  }
+  return v;
+}
+
+struct NormParams {
+  const void *x, *residual;
+  const float *weight;
+  void *residual_out, *out;
+  uint8_t *q8;
+  float *scales;
+  long long ldx, ldr, ldro, ldo;   // row strides in elements
+  int T, H, group, n_groups;       // group: columns per scale, >= H for one scale a row
+  float eps;
+};
+
+// kTpr threads per row, kRows rows per block, kNe elements per thread.
+template <typename T, int kTpr, int kRows, int kNe, bool kVec>
+__global__ void __launch_bounds__(kTpr *kRows) norm_kernel(const NormParams p) {
+  __shared__ float s_red[2][kTpr > 32 ? kTpr / 32 : 1];
+  __shared__ float s_amax[kVec ? 1 : kRows * kNe * (kTpr / 32)];
+  grid_dependency_wait();
+  grid_dependency_launch();
+  const int tid = threadIdx.x % kTpr;
+  const long long row = (long long)blockIdx.x * kRows + threadIdx.x / kTpr;
+  if (kRows > 1 && row >= p.T) return;   // whole warps (kTpr = 32)
+  const int H = p.H;
+  const T *x = static_cast<const T *>(p.x) + row * p.ldx;
+  const T *r = p.residual ? static_cast<const T *>(p.residual) + row * p.ldr : nullptr;
+  T *ro = p.residual_out ? static_cast<T *>(p.residual_out) + row * p.ldro : nullptr;
+  T *out = p.out ? static_cast<T *>(p.out) + row * p.ldo : nullptr;
+  uint8_t *q8 = p.q8 ? p.q8 + row * H : nullptr;
+  float *scales = p.q8 ? p.scales + row * p.n_groups : nullptr;
+
+  float v[kNe];
+  float sq = 0.0f;
+  if (kVec) {
+    constexpr int kNv = kNe / 8;
+    Vec8<T> a[kNv], b[kNv];
+#pragma unroll
+    for (int i = 0; i < kNv; ++i) {
+      const int c = (tid + i * kTpr) * 8;
+      if (c < H) {
+        a[i] = load8(x + c);
+        if (r) b[i] = load8(r + c);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kNv; ++i) {
+      const bool in = (tid + i * kTpr) * 8 < H;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float s = in ? to_f32(a[i].v[j]) : 0.0f;
+        if (r && in) s += to_f32(b[i].v[j]);
+        v[8 * i + j] = s;
+        sq = fmaf(s, s, sq);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kNe; ++i) {
+      const int c = tid + i * kTpr;
+      v[i] = c < H ? to_f32(x[c]) : 0.0f;
+    }
+    if (r) {
+#pragma unroll
+      for (int i = 0; i < kNe; ++i) {
+        const int c = tid + i * kTpr;
+        if (c < H) v[i] += to_f32(r[c]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kNe; ++i) sq = fmaf(v[i], v[i], sq);
+  }
+  if (ro) {
+    if (kVec) {
+#pragma unroll
+      for (int i = 0; i < kNe / 8; ++i) {
+        const int c = (tid + i * kTpr) * 8;
+        Vec8<T> o;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o.v[j] = from_f32<T>(v[8 * i + j]);
+        if (c < H) store8(ro + c, o);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kNe; ++i) {
+        const int c = tid + i * kTpr;
+        if (c < H) ro[c] = from_f32<T>(v[i]);
+      }
+    }
+  }
+  sq = row_reduce<kTpr>(sq, SumOp(), s_red[0], tid);
+  const float inv = __fdiv_rn(1.0f, __fsqrt_rn(sq / (float)H + p.eps));
+
+  // y, and the 16- or 32-bit output
+  if (kVec) {
+#pragma unroll
+    for (int i = 0; i < kNe / 8; ++i) {
+      const int c = (tid + i * kTpr) * 8;
+      if (c < H) {
+        const float4 w0 = __ldg(reinterpret_cast<const float4 *>(p.weight + c));
+        const float4 w1 = __ldg(reinterpret_cast<const float4 *>(p.weight + c + 4));
+        const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        Vec8<T> o;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[8 * i + j] = v[8 * i + j] * inv * w[j];
+          o.v[j] = from_f32<T>(v[8 * i + j]);
+        }
+        if (out) store8(out + c, o);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[8 * i + j] = 0.0f;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kNe; ++i) {
+      const int c = tid + i * kTpr;
+      v[i] = c < H ? v[i] * inv * __ldg(p.weight + c) : 0.0f;
+      if (out && c < H) out[c] = from_f32<T>(v[i]);
+    }
+  }
+  if (!q8) return;
+
+  // e4m3: per group of columns, the largest magnitude, the step and the bytes
+  float row_amax = 0.0f;
+  const bool per_row = p.group >= H;
+  if (per_row) {
+#pragma unroll
+    for (int i = 0; i < kNe; ++i) row_amax = max_nan(row_amax, fabsf(v[i]));
+    row_amax = row_reduce<kTpr>(row_amax, MaxOp(), s_red[1], tid);
+    if (tid == 0) scales[0] = e4m3_step(row_amax);
+  }
+  if (kVec) {
+    const int lanes = p.group / 8;   // lanes per group: 4, 8 or 16
+#pragma unroll
+    for (int i = 0; i < kNe / 8; ++i) {
+      const int c = (tid + i * kTpr) * 8;
+      float amax = row_amax;
+      if (!per_row) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(v[8 * i + j]));
+        for (int o = 1; o < lanes; o <<= 1)
+          amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      }
+      const float step = e4m3_step(amax), mul = __fdiv_rn(1.0f, step);
+      if (c < H) {
+        uint2 q;
+        q.x = e4m3x4(v[8 * i] * mul, v[8 * i + 1] * mul, v[8 * i + 2] * mul, v[8 * i + 3] * mul);
+        q.y = e4m3x4(v[8 * i + 4] * mul, v[8 * i + 5] * mul, v[8 * i + 6] * mul,
+                     v[8 * i + 7] * mul);
+        *reinterpret_cast<uint2 *>(q8 + c) = q;
+        if (!per_row && c % p.group == 0) scales[c / p.group] = step;
+      }
+    }
+  } else {
+    // a warp's 32 lanes hold columns 32 m .. 32 m + 31 of m = i * kTpr / 32 +
+    // warp: the group's magnitude is the largest over its group / 32 such runs
+    float *amax32 = s_amax + (threadIdx.x / kTpr) * kNe * (kTpr / 32);
+    const int per = per_row ? 1 : p.group / 32;
+    if (!per_row) {
+#pragma unroll
+      for (int i = 0; i < kNe; ++i) {
+        float a = fabsf(v[i]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
+        if ((tid & 31) == 0) amax32[i * (kTpr / 32) + (tid >> 5)] = a;
+      }
+      if (kTpr > 32)
+        __syncthreads();
+      else
+        __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < kNe; ++i) {
+      const int c = tid + i * kTpr;
+      if (c >= H) break;
+      float amax = row_amax;
+      if (!per_row) {
+        const int m0 = (c >> 5) / per * per;
+        for (int m = m0; m < m0 + per && m * 32 < H; ++m) amax = max_nan(amax, amax32[m]);
+      }
+      const float step = e4m3_step(amax);
+      q8[c] = __nv_cvt_float_to_fp8(v[i] * __fdiv_rn(1.0f, step), __NV_SATFINITE, __NV_E4M3);
+      if (!per_row && c % p.group == 0) scales[c / p.group] = step;
+    }
+  }
+}
+
+template <typename T, bool kVec>
+cudaError_t launch_norm(const NormParams &p, cudaStream_t stream) {
+  const int H = p.H, T_ = p.T;
+  auto rows = [&](int per) { return dim3(((long long)T_ + per - 1) / per); };
+  if (H <= 256) return launch_pdl(norm_kernel<T, 32, 4, 8, kVec>, rows(4), dim3(128), 0, stream, p);
+  if (H <= 512) return launch_pdl(norm_kernel<T, 32, 4, 16, kVec>, rows(4), dim3(128), 0, stream, p);
+  if (H <= 1024) return launch_pdl(norm_kernel<T, 128, 1, 8, kVec>, rows(1), dim3(128), 0, stream, p);
+  if (H <= 2048) return launch_pdl(norm_kernel<T, 256, 1, 8, kVec>, rows(1), dim3(256), 0, stream, p);
+  if (H <= 4096) return launch_pdl(norm_kernel<T, 256, 1, 16, kVec>, rows(1), dim3(256), 0, stream, p);
+  if (H <= 8192) return launch_pdl(norm_kernel<T, 512, 1, 16, kVec>, rows(1), dim3(512), 0, stream, p);
+  return launch_pdl(norm_kernel<T, 1024, 1, 16, kVec>, rows(1), dim3(1024), 0, stream, p);
+}
+
+// ---------------------------------------------------------------- gradient
+struct NormGradParams {
+  const void *h, *dout, *dsum;
+  const float *weight;
+  void *dx;
+  float *partial;                // [gridDim.x][H] sums over each block's rows, or null
+  long long ldh, lddo, ldds, lddx;
+  int T, H;
+  float eps;
+};
+
+// One block walks rows blockIdx.x, + gridDim.x, ...; a thread keeps its
+// columns' weight-gradient sums in registers over all of them.
+template <typename T, int kTpr, int kNe, bool kVec>
+__global__ void __launch_bounds__(kTpr) norm_grad_kernel(const NormGradParams p) {
+  __shared__ float s_red[2][2][kTpr / 32];
+  grid_dependency_wait();
+  grid_dependency_launch();
+  const int tid = threadIdx.x, H = p.H;
+  auto col = [&](int i) { return kVec ? (tid + (i / 8) * kTpr) * 8 + i % 8 : tid + i * kTpr; };
+  float dg[kNe];
+#pragma unroll
+  for (int i = 0; i < kNe; ++i) dg[i] = 0.0f;
+  int flip = 0;
+  for (long long row = blockIdx.x; row < p.T; row += gridDim.x, flip ^= 1) {
+    const T *h = static_cast<const T *>(p.h) + row * p.ldh;
+    const T *dy = static_cast<const T *>(p.dout) + row * p.lddo;
+    const T *ds = p.dsum ? static_cast<const T *>(p.dsum) + row * p.ldds : nullptr;
+    T *dx = static_cast<T *>(p.dx) + row * p.lddx;
+    float a[kNe], d[kNe];
+    if (kVec) {
+#pragma unroll
+      for (int i = 0; i < kNe; i += 8) {
+        const int c = col(i);
+        Vec8<T> ha, da;
+        if (c < H) {
+          ha = load8(h + c);
+          da = load8(dy + c);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          a[i + j] = c < H ? to_f32(ha.v[j]) : 0.0f;
+          d[i + j] = c < H ? to_f32(da.v[j]) : 0.0f;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kNe; ++i) {
+        const int c = col(i);
+        a[i] = c < H ? to_f32(h[c]) : 0.0f;
+        d[i] = c < H ? to_f32(dy[c]) : 0.0f;
+      }
+    }
+    float sq = 0.0f, dot = 0.0f;
+    float w[kNe];
+#pragma unroll
+    for (int i = 0; i < kNe; ++i) {
+      const int c = col(i);
+      w[i] = c < H ? __ldg(p.weight + c) : 0.0f;
+      sq = fmaf(a[i], a[i], sq);
+      dot = fmaf(d[i] * w[i], a[i], dot);
+    }
+    sq = row_reduce<kTpr>(sq, SumOp(), s_red[flip][0], tid);
+    dot = row_reduce<kTpr>(dot, SumOp(), s_red[flip][1], tid);
+    const float inv = __fdiv_rn(1.0f, __fsqrt_rn(sq / (float)H + p.eps));
+    const float back = dot * inv * inv / (float)H;   // i^2 mean(gy h)
+    float o[kNe];
+#pragma unroll
+    for (int i = 0; i < kNe; ++i) {
+      dg[i] = fmaf(d[i], a[i] * inv, dg[i]);
+      o[i] = inv * (d[i] * w[i] - a[i] * back);
+    }
+    if (kVec) {
+#pragma unroll
+      for (int i = 0; i < kNe; i += 8) {
+        const int c = col(i);
+        if (c < H) {
+          Vec8<T> e, s;
+          if (ds) s = load8(ds + c);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            e.v[j] = from_f32<T>(ds ? o[i + j] + to_f32(s.v[j]) : o[i + j]);
+          store8(dx + c, e);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kNe; ++i) {
+        const int c = col(i);
+        if (c < H) dx[c] = from_f32<T>(ds ? o[i] + to_f32(ds[c]) : o[i]);
+      }
+    }
+  }
+  if (p.partial) {
+    float *out = p.partial + (long long)blockIdx.x * H;
+#pragma unroll
+    for (int i = 0; i < kNe; ++i) {
+      const int c = col(i);
+      if (c < H) out[c] = dg[i];
+    }
+  }
+}
+
+// Sum of n rows of partial sums, in a fixed order: 32 columns a block, 8 row
+// lanes.
+__global__ void __launch_bounds__(256) norm_grad_sum_kernel(const float *partial, int n, int H,
+                                                            float *out) {
+  __shared__ float s[8][33];
+  grid_dependency_wait();
+  grid_dependency_launch();
+  const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float v = 0.0f;
+  if (c < H)
+    for (int r = y; r < n; r += 8) v += partial[(long long)r * H + c];
+  s[y][lane] = v;
+  __syncthreads();
+  if (y == 0 && c < H) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) v += s[i][lane];
+    out[c] = v;
+  }
+}
+
+// Blocks of the gradient kernel: enough for every multiprocessor (148) twice
+// at the most.
+constexpr int kGradBlocks = 296;
+inline int grad_blocks(int T) { return T < kGradBlocks ? T : kGradBlocks; }
+
+template <typename T, bool kVec>
+cudaError_t launch_norm_grad(const NormGradParams &p, cudaStream_t stream) {
+  const dim3 grid(grad_blocks(p.T));
+  if (p.H <= 512) return launch_pdl(norm_grad_kernel<T, 64, 8, kVec>, grid, dim3(64), 0, stream, p);
+  if (p.H <= 1024) return launch_pdl(norm_grad_kernel<T, 128, 8, kVec>, grid, dim3(128), 0, stream, p);
+  if (p.H <= 2048) return launch_pdl(norm_grad_kernel<T, 256, 8, kVec>, grid, dim3(256), 0, stream, p);
+  if (p.H <= 4096) return launch_pdl(norm_grad_kernel<T, 512, 8, kVec>, grid, dim3(512), 0, stream, p);
+  if (p.H <= 8192) return launch_pdl(norm_grad_kernel<T, 1024, 8, kVec>, grid, dim3(1024), 0, stream, p);
+  return launch_pdl(norm_grad_kernel<T, 1024, 16, kVec>, grid, dim3(1024), 0, stream, p);
+}
+
+int dtype_bytes(int dtype) {
+  switch (dtype) {
+    case STRATA_DTYPE_BF16: case STRATA_DTYPE_F16: return 2;
+    case STRATA_DTYPE_F32: return 4;
+  }
+  return 0;
+}
+
+inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// A row operand: present, aligned to its elements, rows that do not overlap.
+bool rows_ok(const void *p, long long ld, int T, int H, int bytes) {
+  return p && aligned(p, bytes) && (T <= 1 || ld >= H);
+}
+// ... that 16-byte accesses can walk.
+bool rows_vec(const void *p, long long ld, int bytes) {
+  return !p || (aligned(p, 16) && ld * bytes % 16 == 0);
+}
+
+}  // namespace
+
+}  // namespace strata
+
+using namespace strata;
+
+extern "C" {
+
+strata_status strata_rmsnorm(int dtype, const void *x, long long x_stride, const void *residual,
+                             long long residual_stride, const float *weight, float eps,
+                             int n_tokens, int hidden, void *residual_out,
+                             long long residual_out_stride, void *out, long long out_stride,
+                             void *out_q8, float *scales, int group, strata_stream_t stream) {
+  const int b = dtype_bytes(dtype);
+  if (!b || n_tokens < 0 || hidden < 1 || !(eps >= 0.0f) || !(eps <= 3.0e38f))
+    return STRATA_ERR_INVALID_ARG;
+  if (hidden > kNormMaxH) return STRATA_ERR_UNSUPPORTED;
+  if (out_q8 ? !scales || (group != 32 && group != 64 && group != 128 && group < hidden)
+             : scales != nullptr)
+    return STRATA_ERR_INVALID_ARG;
+  if (n_tokens == 0) return STRATA_OK;
+  if (!rows_ok(x, x_stride, n_tokens, hidden, b) || !weight || !aligned(weight, 4) ||
+      !aligned(scales, 4) || (!out && !out_q8))
+    return STRATA_ERR_INVALID_ARG;
+  if ((residual && !rows_ok(residual, residual_stride, n_tokens, hidden, b)) ||
+      (residual_out && !rows_ok(residual_out, residual_out_stride, n_tokens, hidden, b)) ||
+      (out && !rows_ok(out, out_stride, n_tokens, hidden, b)))
+    return STRATA_ERR_INVALID_ARG;
+  NormParams p;
+  p.x = x;
+  p.residual = residual;
+  p.weight = weight;
+  p.residual_out = residual_out;
+  p.out = out;
+  p.q8 = static_cast<uint8_t *>(out_q8);
+  p.scales = scales;
+  p.ldx = x_stride;
+  p.ldr = residual_stride;
+  p.ldro = residual_out_stride;
+  p.ldo = out_stride;
+  p.T = n_tokens;
+  p.H = hidden;
+  p.group = out_q8 ? group : hidden;
+  p.n_groups = (hidden + p.group - 1) / p.group;
+  p.eps = eps;
+  const bool vec = hidden % 8 == 0 && rows_vec(x, x_stride, b) &&
+                   rows_vec(residual, residual_stride, b) &&
+                   rows_vec(residual_out, residual_out_stride, b) && rows_vec(out, out_stride, b) &&
+                   aligned(weight, 16) && aligned(out_q8, 8);
+  cudaError_t e;
+  switch (dtype) {
+    case STRATA_DTYPE_BF16:
+      e = vec ? launch_norm<__nv_bfloat16, true>(p, stream) : launch_norm<__nv_bfloat16, false>(p, stream);
+      break;
+    case STRATA_DTYPE_F16:
+      e = vec ? launch_norm<__half, true>(p, stream) : launch_norm<__half, false>(p, stream);
+      break;
+    default:
+      e = vec ? launch_norm<float, true>(p, stream) : launch_norm<float, false>(p, stream);
+  }
+  return status_of(e);
+}
+
+size_t strata_rmsnorm_backward_workspace(int n_tokens, int hidden) {
+  if (n_tokens < 0 || hidden < 1 || hidden > kNormMaxH) return 0;
+  const size_t blocks = grad_blocks(n_tokens > 0 ? n_tokens : 1);
+  return blocks * hidden * sizeof(float);
+}
+
+strata_status strata_rmsnorm_backward(int dtype, const void *h, long long h_stride,
+                                      const float *weight, float eps, const void *dout,
+                                      long long dout_stride, const void *dsum,
+                                      long long dsum_stride, int n_tokens, int hidden, void *dx,
+                                      long long dx_stride, float *dweight, void *workspace,
+                                      size_t workspace_bytes, strata_stream_t stream) {
+  const int b = dtype_bytes(dtype);
+  if (!b || n_tokens < 0 || hidden < 1 || !(eps >= 0.0f) || !(eps <= 3.0e38f))
+    return STRATA_ERR_INVALID_ARG;
+  if (hidden > kNormMaxH) return STRATA_ERR_UNSUPPORTED;
+  if (!aligned(dweight, 4)) return STRATA_ERR_INVALID_ARG;
+  if (n_tokens == 0)
+    return dweight ? status_of(cudaMemsetAsync(dweight, 0, sizeof(float) * hidden, stream)) : STRATA_OK;
+  if (!rows_ok(h, h_stride, n_tokens, hidden, b) || !weight || !aligned(weight, 4) ||
+      !rows_ok(dout, dout_stride, n_tokens, hidden, b) ||
+      (dsum && !rows_ok(dsum, dsum_stride, n_tokens, hidden, b)) ||
+      !rows_ok(dx, dx_stride, n_tokens, hidden, b))
+    return STRATA_ERR_INVALID_ARG;
+  if (dweight && (!workspace || !aligned(workspace, 16) ||
+                  workspace_bytes < strata_rmsnorm_backward_workspace(n_tokens, hidden)))
+    return STRATA_ERR_INVALID_ARG;
+  NormGradParams p;
+  p.h = h;
+  p.dout = dout;
+  p.dsum = dsum;
+  p.weight = weight;
+  p.dx = dx;
+  p.partial = dweight ? static_cast<float *>(workspace) : nullptr;
+  p.ldh = h_stride;
+  p.lddo = dout_stride;
+  p.ldds = dsum_stride;
+  p.lddx = dx_stride;
+  p.T = n_tokens;
+  p.H = hidden;
+  p.eps = eps;
+  const bool vec = hidden % 8 == 0 && rows_vec(h, h_stride, b) && rows_vec(dout, dout_stride, b) &&
+                   rows_vec(dsum, dsum_stride, b) && rows_vec(dx, dx_stride, b);
+  cudaError_t e;
+  switch (dtype) {
+    case STRATA_DTYPE_BF16:
+      e = vec ? launch_norm_grad<__nv_bfloat16, true>(p, stream)
+              : launch_norm_grad<__nv_bfloat16, false>(p, stream);
+      break;
+    case STRATA_DTYPE_F16:
+      e = vec ? launch_norm_grad<__half, true>(p, stream) : launch_norm_grad<__half, false>(p, stream);
+      break;
+    default:
+      e = vec ? launch_norm_grad<float, true>(p, stream) : launch_norm_grad<float, false>(p, stream);
+  }
+  if (e == cudaSuccess && dweight)
+    e = launch_pdl(norm_grad_sum_kernel, dim3((hidden + 31) / 32), dim3(256), 0, stream,
+                   (const float *)p.partial, grad_blocks(n_tokens), hidden, dweight);
+  return status_of(e);
+}
+
+}  // extern "C"
