@@ -429,6 +429,90 @@ strata_status strata_rmsnorm_backward(int dtype, const void *h, long long h_stri
                                       long long dx_stride, float *dweight, void *workspace,
                                       size_t workspace_bytes, strata_stream_t stream);
 
+/* ---- Training the router over frozen experts.  The pages describe no
+ * training; these calls go with strata_moe_route, whose logits and idx they
+ * take.  They keep nothing in the handle but the device status word, run on the
+ * handle's device (which must be the current one) and use the caller's
+ * workspace: device memory, 16-byte aligned, of at least the size that the
+ * *_workspace call gives for the same arguments, written before it is read.
+ * Calls that may overlap on the GPU, and graphs that may be replayed at once,
+ * need a workspace each.  At most 2^28 tokens and sequences a call.
+ *
+ * Balance loss of a batch's routing, and how many tokens each expert got.
+ * logits: device fp32 [n_tokens][n_experts]; idx: device int32
+ * [n_tokens][top_k] (both from strata_moe_route; an expert named twice by a
+ * token counts twice).  The tokens may be n_seq sequences packed one behind
+ * the other: seq_off, device int32 [n_seq + 1], not decreasing, sequence b
+ * holding tokens seq_off[b] .. seq_off[b + 1] - 1 (empty ones are allowed;
+ * tokens outside every sequence do not count).  seq_off NULL: n_seq must be 1,
+ * one sequence of all tokens.  mask: device bytes [n_tokens], zero for tokens
+ * that do not count (padding; their logits and ids may hold anything), or NULL.
+ * With p[t] = softmax(logits[t]) over all experts or, with
+ * STRATA_ROUTE_SIGMOID, the sigmoid scores divided by their sum (no correction
+ * bias, no routed scale), and n_b tokens of sequence b counting:
+ *     counts[b][e] = pairs (t, j) with idx[t][j] = e
+ *     loss = coef / n_seq * sum_b sum_e (counts[b][e] n_experts / (top_k n_b))
+ *                                       * (sum_t p[t][e] / n_b)
+ * A sequence with no counting token adds nothing; a row of logits that are all
+ * -inf has no probabilities (zeros).  counts: device int32 [n_seq][n_experts];
+ * tokens: device int32 [n_seq], the n_b; loss: device fp32 [1].  Sums are taken
+ * in fp32 within a block of tokens and in double across blocks, in a fixed
+ * order.  n_tokens == 0 zeroes the outputs.  Asynchronous on `stream`.
+ * Host errors: INVALID_ARG, CUDA.  Device errors (strata_moe_get_status):
+ * DEVICE_STATUS (bit 2: an id of a counting token outside [0, n_experts), not
+ * counted; bit 8: seq_off decreasing or outside [0, n_tokens], the sequence's
+ * span is clamped). */
+size_t strata_moe_balance_workspace(const strata_moe *h, int n_tokens, int n_seq);
+strata_status strata_moe_balance(strata_moe *h, const float *logits, const int32_t *idx,
+                                 int n_tokens, const int32_t *seq_off, int n_seq,
+                                 const uint8_t *mask, float coef, int32_t *counts, int32_t *tokens,
+                                 float *loss, void *workspace, size_t workspace_bytes,
+                                 strata_stream_t stream);
+
+/* Gradient of the balance loss in the logits (the counts are constants):
+ * with f_e = counts[b][e] n_experts / (top_k n_b) and
+ * u = dloss coef / (n_seq n_b),
+ *     softmax: dlogits[t][e] = u p_e (f_e - sum_j f_j p_j)
+ *     sigmoid: dlogits[t][e] = u s_e (1 - s_e) / S (f_e - sum_j f_j p_j)
+ * and zero for tokens that do not count (masked, or outside every sequence).
+ * counts and tokens: as strata_moe_balance wrote them; dloss: device fp32 [1],
+ * or NULL for 1; dlogits: device fp32 [n_tokens][n_experts], not logits.  No
+ * workspace.  Errors: INVALID_ARG, CUDA. */
+strata_status strata_moe_balance_backward(strata_moe *h, const float *logits, int n_tokens,
+                                          const int32_t *seq_off, int n_seq, const uint8_t *mask,
+                                          float coef, const int32_t *counts, const int32_t *tokens,
+                                          const float *dloss, float *dlogits,
+                                          strata_stream_t stream);
+
+/* Gradient of the routing: from the gradients of its outputs to the router's
+ * weights and its input.  x_bf16, logits, idx: the input and outputs of
+ * strata_moe_route.  dw: device fp32 [n_tokens][top_k], gradient of the routing
+ * weights w, or NULL; dlogits: device fp32 [n_tokens][n_experts], gradient of
+ * the logits (e.g. of the balance loss), or NULL; one of them must be given.
+ * logits and idx are read only where dw is given.  With
+ *     dl = dlogits + (dw through w: of the softmax over the selected logits
+ *          w_j (dw_j - sum_i w_i dw_i); with STRATA_ROUTE_SIGMOID, S the sum of
+ *          the selected scores, routed_scale s_j (1 - s_j) / S
+ *          (dw_j - sum_i s_i / S dw_i)), added at idx_j
+ * (the selection itself and the correction bias have no gradient):
+ *     dW = dl^T x   device fp32 [n_experts][hidden], or NULL
+ *     db = sum of dl over the tokens   device fp32 [n_experts], or NULL
+ *     dx = dl W     device bf16 [n_tokens][hidden], or NULL (needs set_router)
+ * each overwritten, not added to.  A row of dl that is zero still multiplies
+ * its x: rows of x must be finite.  An expert named twice by a token gets both
+ * terms.  x, dW, dx 16-byte aligned, workspace 256-byte aligned.  Products are
+ * taken to fp32 accuracy (dW) or to well below the rounding of bf16 (dx), sums
+ * in fp32 in a fixed order.  n_tokens == 0 zeroes dW and db.
+ * Host errors: INVALID_ARG, CUDA.  Device errors: DEVICE_STATUS (bit 2: an id
+ * outside [0, n_experts); that token's dw is ignored, as the forward's output
+ * for it is zero). */
+size_t strata_moe_route_backward_workspace(const strata_moe *h, int n_tokens);
+strata_status strata_moe_route_backward(strata_moe *h, const void *x_bf16, int n_tokens,
+                                        const float *logits, const int32_t *idx, const float *dw,
+                                        const float *dlogits, float *dW, float *db, void *dx_bf16,
+                                        void *workspace, size_t workspace_bytes,
+                                        strata_stream_t stream);
+
 /* Human-readable name of a status. */
 const char *strata_status_str(strata_status s);
 

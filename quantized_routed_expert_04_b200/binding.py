@@ -81,6 +81,11 @@ def load_library():
             "strata_rmsnorm": (I, [I, P, L, P, L, P, F, I, I, P, L, P, L, P, P, I, P]),
             "strata_rmsnorm_backward_workspace": (Z, [I, I]),
             "strata_rmsnorm_backward": (I, [I, P, L, P, F, P, L, P, L, I, I, P, L, P, P, Z, P]),
+            "strata_moe_balance_workspace": (Z, [P, I, I]),
+            "strata_moe_balance": (I, [P, P, P, I, P, I, P, F, P, P, P, P, Z, P]),
+            "strata_moe_balance_backward": (I, [P, P, I, P, I, P, F, P, P, P, P, P]),
+            "strata_moe_route_backward_workspace": (Z, [P, I]),
+            "strata_moe_route_backward": (I, [P, P, I, P, P, P, P, P, P, P, P, Z, P]),
             "strata_status_str": (ctypes.c_char_p, [I]),
             "strata_arena_create": (I, [P, P, P, ctypes.POINTER(P)]),
             "strata_arena_destroy": (None, [P]),
@@ -326,6 +331,38 @@ def _workspace(t, like, where):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
+def strata_moe_balance_workspace(h, n_tokens, n_seq=1):
+    return int(_load().strata_moe_balance_workspace(h, n_tokens, n_seq))
+
+
+def strata_moe_balance(h, logits, idx, n_tokens, coef, counts, tokens, loss, workspace,
+                       workspace_bytes, seq_off=None, n_seq=1, mask=None, stream=None):
+    _check(_load().strata_moe_balance(h, _addr(logits), _addr(idx), n_tokens, _addr(seq_off),
+                                      n_seq, _addr(mask), coef, _addr(counts), _addr(tokens),
+                                      _addr(loss), _addr(workspace), workspace_bytes,
+                                      _stream(stream)), "strata_moe_balance")
+
+
+def strata_moe_balance_backward(h, logits, n_tokens, coef, counts, tokens, dlogits, dloss=None,
+                                seq_off=None, n_seq=1, mask=None, stream=None):
+    _check(_load().strata_moe_balance_backward(h, _addr(logits), n_tokens, _addr(seq_off), n_seq,
+                                               _addr(mask), coef, _addr(counts), _addr(tokens),
+                                               _addr(dloss), _addr(dlogits), _stream(stream)),
+           "strata_moe_balance_backward")
+
+
+def strata_moe_route_backward_workspace(h, n_tokens):
+    return int(_load().strata_moe_route_backward_workspace(h, n_tokens))
+
+
+def strata_moe_route_backward(h, x, n_tokens, logits, idx, dw, dlogits, dW, db, dx, workspace,
+                              workspace_bytes, stream=None):
+    _check(_load().strata_moe_route_backward(h, _addr(x), n_tokens, _addr(logits), _addr(idx),
+                                             _addr(dw), _addr(dlogits), _addr(dW), _addr(db),
+                                             _addr(dx), _addr(workspace), workspace_bytes,
+                                             _stream(stream)), "strata_moe_route_backward")
+
+
 def strata_status_str(st):
     return _load().strata_status_str(int(st)).decode()
 
@@ -451,6 +488,50 @@ class StrataMoE:
 
     def forward_noalloc(self, x, out, stream=None):
         strata_moe_forward_noalloc(self.h, x, x.shape[0], out, stream)
+
+    # Training the router.  These methods take torch tensors and check that
+    # their sizes go together (StrataError, INVALID_ARG); `workspace` is a
+    # buffer of the size that the *_workspace method gives, kept by the caller.
+    def balance_workspace(self, n_tokens, n_seq=1):
+        return strata_moe_balance_workspace(self.h, n_tokens, n_seq)
+
+    def _balance_args(self, logits, counts, tokens, seq_off, mask, where):
+        T, E = logits.shape[0], self.n_experts
+        n_seq = 1 if seq_off is None else seq_off.numel() - 1
+        _on_current(logits, where)
+        return (T, n_seq, _flat(logits, logits, T * E, 4, where),
+                _flat(counts, logits, n_seq * E, 4, where), _flat(tokens, logits, n_seq, 4, where),
+                _flat(seq_off, logits, n_seq + 1, 4, where), _flat(mask, logits, T, 1, where))
+
+    def balance(self, logits, idx, coef, counts, tokens, loss, workspace, seq_off=None, mask=None,
+                stream=None):
+        w = "strata_moe_balance"
+        T, n_seq, la, ca, ta, sa, ma = self._balance_args(logits, counts, tokens, seq_off, mask, w)
+        ws, nws = _workspace(workspace, logits, w)
+        strata_moe_balance(self.h, la, _flat(idx, logits, T * self.top_k, 4, w), T, coef, ca, ta,
+                           _flat(loss, logits, 1, 4, w), ws, nws, sa, n_seq, ma, stream)
+
+    def balance_backward(self, logits, coef, counts, tokens, dlogits, dloss=None, seq_off=None,
+                         mask=None, stream=None):
+        w = "strata_moe_balance_backward"
+        T, n_seq, la, ca, ta, sa, ma = self._balance_args(logits, counts, tokens, seq_off, mask, w)
+        strata_moe_balance_backward(self.h, la, T, coef, ca, ta,
+                                    _flat(dlogits, logits, T * self.n_experts, 4, w),
+                                    _flat(dloss, logits, 1, 4, w), sa, n_seq, ma, stream)
+
+    def route_backward_workspace(self, n_tokens):
+        return strata_moe_route_backward_workspace(self.h, n_tokens)
+
+    def route_backward(self, x, logits, idx, dw, dlogits, dW, db, dx, workspace, stream=None):
+        w = "strata_moe_route_backward"
+        T, E, k, H = x.shape[0], self.n_experts, self.top_k, self.hidden
+        _on_current(x, w)
+        ws, nws = _workspace(workspace, x, w)
+        strata_moe_route_backward(self.h, _flat(x, x, T * H, 2, w), T,
+                                  _flat(logits, x, T * E, 4, w), _flat(idx, x, T * k, 4, w),
+                                  _flat(dw, x, T * k, 4, w), _flat(dlogits, x, T * E, 4, w),
+                                  _flat(dW, x, E * H, 4, w), _flat(db, x, E, 4, w),
+                                  _flat(dx, x, T * H, 2, w), ws, nws, stream)
 
     def status(self, stream=None):
         return strata_moe_get_status(self.h, stream)

@@ -109,4 +109,50 @@ __global__ void gather_rows_kernel(const __half *x16, const int *pair_tok, const
 size_t tc_smem_bytes();
 int tc_threads();
 
+// ---- balance loss of a batch's routing (balance.cu)
+struct BalanceParams {
+  const float *logits;     // [T][E]
+  const int32_t *idx;      // [T][k]
+  const int32_t *seq_off;  // [n_seq + 1], or null: one sequence of all T tokens
+  const uint8_t *mask;     // [T], or null: every token counts
+  int T, E, k, n_seq;
+  int sigmoid;             // scores divided by their sum instead of softmax
+  float coef;
+  int32_t *counts;         // [n_seq][E]
+  int32_t *tokens;         // [n_seq]
+  float *loss;             // [1]
+  int *status;
+  // set by run_balance / run_balance_grad
+  int chunk;               // tokens per block
+  float *part_p;           // [blocks + n_seq][E] sums of p per piece
+  int *part_cnt, *part_tok;
+  double *seq_loss;        // [n_seq]
+};
+struct BalanceGradParams {
+  BalanceParams p;         // counts and tokens are inputs; no idx, loss
+  const float *dloss;      // [1], or null: 1
+  float *dlogits;          // [T][E]
+};
+size_t balance_workspace(int T, int E, int n_seq);
+cudaError_t run_balance(BalanceParams p, void *workspace, cudaStream_t stream);
+cudaError_t run_balance_grad(BalanceGradParams g, cudaStream_t stream);
+
+// ---- gradient of the router (route_grad.cu)
+struct RouteGradParams {
+  const __nv_bfloat16 *x;  // [T][H]
+  const float *W;          // [E][H]
+  const float *logits;     // [T][E], read where dw is given
+  const int32_t *idx;      // [T][k], read where dw is given
+  const float *dw;         // [T][k] or null
+  const float *dlogits;    // [T][E] or null
+  int T, H, E, k;
+  RouteMode mode;
+  float *dW, *db;          // [E][H], [E], or null
+  __nv_bfloat16 *dx;       // [T][H] or null
+  int *status;
+  float *dl;               // set by run_route_grad
+};
+size_t route_grad_workspace(int T, int E, int H);
+cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stream);
+
 }  // namespace strata

@@ -767,6 +767,171 @@ strata_status strata_moe_profile_read(strata_moe *h, int n_phases, int *launches
 }  // extern "C"
 
 // ---------------------------------------------------------------------------
+// Training the router: balance loss and the router's gradient.  These calls
+// keep nothing in the handle: their workspaces are the caller's.
+
+namespace {
+
+// Tokens (and sequences) of one training call: token numbers and block offsets
+// stay well inside 32 bits.
+constexpr int kMaxTrainTokens = 1 << 28;
+
+inline bool misaligned(const void *p, size_t a) {
+  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0;
+}
+
+// The kernels run on the handle's device, which must be the current one.
+strata_status check_device(const strata_moe *h) {
+  int device = -1;
+  if (cudaGetDevice(&device) != cudaSuccess) return STRATA_ERR_CUDA;
+  return device == h->device ? STRATA_OK : STRATA_ERR_INVALID_ARG;
+}
+
+strata_status check_balance(const strata_moe *h, const float *logits, int T, const int32_t *seq_off,
+                            int n_seq, float coef, const int32_t *counts, const int32_t *tokens) {
+  if (!h || T < 0 || T > kMaxTrainTokens || n_seq < 1 || n_seq > kMaxTrainTokens ||
+      (!seq_off && n_seq != 1))
+    return STRATA_ERR_INVALID_ARG;
+  if (!(coef >= -3.0e38f) || !(coef <= 3.0e38f)) return STRATA_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || misaligned(logits, 4))) return STRATA_ERR_INVALID_ARG;
+  if (misaligned(seq_off, 4) || !counts || misaligned(counts, 4) || !tokens ||
+      misaligned(tokens, 4))
+    return STRATA_ERR_INVALID_ARG;
+  return STRATA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t strata_moe_balance_workspace(const strata_moe *h, int n_tokens, int n_seq) {
+  if (!h || n_tokens < 0 || n_tokens > kMaxTrainTokens || n_seq < 1 || n_seq > kMaxTrainTokens)
+    return 0;
+  return balance_workspace(n_tokens, h->E, n_seq);
+}
+
+strata_status strata_moe_balance(strata_moe *h, const float *logits, const int32_t *idx,
+                                 int n_tokens, const int32_t *seq_off, int n_seq,
+                                 const uint8_t *mask, float coef, int32_t *counts, int32_t *tokens,
+                                 float *loss, void *workspace, size_t workspace_bytes,
+                                 strata_stream_t stream) {
+  strata_status st = check_balance(h, logits, n_tokens, seq_off, n_seq, coef, counts, tokens);
+  if (st != STRATA_OK) return st;
+  if (!loss || misaligned(loss, 4)) return STRATA_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (!idx || misaligned(idx, 4) || !workspace || misaligned(workspace, 16) ||
+                       workspace_bytes < balance_workspace(n_tokens, h->E, n_seq)))
+    return STRATA_ERR_INVALID_ARG;
+  st = check_device(h);
+  if (st != STRATA_OK) return st;
+  if (n_tokens == 0) {
+    cudaError_t e = cudaMemsetAsync(counts, 0, sizeof(int32_t) * (size_t)n_seq * h->E, stream);
+    if (e == cudaSuccess) e = cudaMemsetAsync(tokens, 0, sizeof(int32_t) * n_seq, stream);
+    if (e == cudaSuccess) e = cudaMemsetAsync(loss, 0, sizeof(float), stream);
+    return cuda_status(e);
+  }
+  BalanceParams p;
+  std::memset(&p, 0, sizeof p);
+  p.logits = logits;
+  p.idx = idx;
+  p.seq_off = seq_off;
+  p.mask = mask;
+  p.T = n_tokens;
+  p.E = h->E;
+  p.k = h->k;
+  p.n_seq = n_seq;
+  p.sigmoid = h->mode.sigmoid;
+  p.coef = coef;
+  p.counts = counts;
+  p.tokens = tokens;
+  p.loss = loss;
+  p.status = h->status;
+  return cuda_status(run_balance(p, workspace, stream));
+}
+
+strata_status strata_moe_balance_backward(strata_moe *h, const float *logits, int n_tokens,
+                                          const int32_t *seq_off, int n_seq, const uint8_t *mask,
+                                          float coef, const int32_t *counts, const int32_t *tokens,
+                                          const float *dloss, float *dlogits,
+                                          strata_stream_t stream) {
+  strata_status st = check_balance(h, logits, n_tokens, seq_off, n_seq, coef, counts, tokens);
+  if (st != STRATA_OK) return st;
+  if (misaligned(dloss, 4)) return STRATA_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (!dlogits || misaligned(dlogits, 4))) return STRATA_ERR_INVALID_ARG;
+  st = check_device(h);
+  if (st != STRATA_OK) return st;
+  if (n_tokens == 0) return STRATA_OK;
+  BalanceGradParams g;
+  std::memset(&g, 0, sizeof g);
+  g.p.logits = logits;
+  g.p.seq_off = seq_off;
+  g.p.mask = mask;
+  g.p.T = n_tokens;
+  g.p.E = h->E;
+  g.p.k = h->k;
+  g.p.n_seq = n_seq;
+  g.p.sigmoid = h->mode.sigmoid;
+  g.p.coef = coef;
+  g.p.counts = const_cast<int32_t *>(counts);
+  g.p.tokens = const_cast<int32_t *>(tokens);
+  g.dloss = dloss;
+  g.dlogits = dlogits;
+  return cuda_status(run_balance_grad(g, stream));
+}
+
+size_t strata_moe_route_backward_workspace(const strata_moe *h, int n_tokens) {
+  if (!h || n_tokens < 0 || n_tokens > kMaxTrainTokens) return 0;
+  return route_grad_workspace(n_tokens, h->E, h->H);
+}
+
+strata_status strata_moe_route_backward(strata_moe *h, const void *x_bf16, int n_tokens,
+                                        const float *logits, const int32_t *idx, const float *dw,
+                                        const float *dlogits, float *dW, float *db, void *dx_bf16,
+                                        void *workspace, size_t workspace_bytes,
+                                        strata_stream_t stream) {
+  if (!h || n_tokens < 0 || n_tokens > kMaxTrainTokens || (!dW && !db && !dx_bf16))
+    return STRATA_ERR_INVALID_ARG;
+  if (misaligned(dW, 16) || misaligned(db, 4) || misaligned(dx_bf16, 16)) return STRATA_ERR_INVALID_ARG;
+  if (n_tokens > 0) {
+    if ((!dw && !dlogits) || (dw && (!logits || !idx))) return STRATA_ERR_INVALID_ARG;
+    if (misaligned(logits, 4) || misaligned(idx, 4) || misaligned(dw, 4) || misaligned(dlogits, 4))
+      return STRATA_ERR_INVALID_ARG;
+    if ((dW && (!x_bf16 || misaligned(x_bf16, 16))) || (dx_bf16 && !h->router_W))
+      return STRATA_ERR_INVALID_ARG;
+    if (!workspace || misaligned(workspace, 256) ||
+        workspace_bytes < route_grad_workspace(n_tokens, h->E, h->H))
+      return STRATA_ERR_INVALID_ARG;
+  }
+  strata_status st = check_device(h);
+  if (st != STRATA_OK) return st;
+  if (n_tokens == 0) {
+    cudaError_t e = cudaSuccess;
+    if (dW) e = cudaMemsetAsync(dW, 0, sizeof(float) * (size_t)h->E * h->H, stream);
+    if (e == cudaSuccess && db) e = cudaMemsetAsync(db, 0, sizeof(float) * h->E, stream);
+    return cuda_status(e);
+  }
+  RouteGradParams p;
+  std::memset(&p, 0, sizeof p);
+  p.x = static_cast<const __nv_bfloat16 *>(x_bf16);
+  p.W = h->router_W;
+  p.logits = logits;
+  p.idx = idx;
+  p.dw = dw;
+  p.dlogits = dlogits;
+  p.T = n_tokens;
+  p.H = h->H;
+  p.E = h->E;
+  p.k = h->k;
+  p.mode = h->mode;
+  p.dW = dW;
+  p.db = db;
+  p.dx = static_cast<__nv_bfloat16 *>(dx_bf16);
+  p.status = h->status;
+  return cuda_status(run_route_grad(p, workspace, stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
 // strata_moe_forward_noalloc: the small-batch forward with its workspace in a
 // fixed device array of this file instead of the handle's growable
 // allocation.  It is for callers that may not allocate device memory at the
