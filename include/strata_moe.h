@@ -429,6 +429,30 @@ strata_status strata_rmsnorm_backward(int dtype, const void *h, long long h_stri
                                       long long dx_stride, float *dweight, void *workspace,
                                       size_t workspace_bytes, strata_stream_t stream);
 
+/* The layer with its norm in front: s = x + residual, x' = norm(s) as
+ * strata_rmsnorm in bf16, then strata_moe_forward of x'.  x_bf16,
+ * residual_bf16 (or NULL), residual_out_bf16 (or NULL), normed_bf16 (receives
+ * x', 16-byte aligned; it is also the x of strata_moe_route_backward) and
+ * out_bf16: device bf16 [n_tokens][hidden], contiguous; out must be none of the
+ * other outputs.  residual_out may be x or residual.  Runs on the handle's
+ * device, which must be the current one.  Errors: those of strata_rmsnorm and
+ * strata_moe_forward. */
+strata_status strata_moe_forward_norm(strata_moe *h, const void *x_bf16, const void *residual_bf16,
+                                      const float *weight, float eps, int n_tokens,
+                                      void *residual_out_bf16, void *normed_bf16, void *out_bf16,
+                                      strata_stream_t stream);
+
+/* The layer on activations in 8 bits, as strata_rmsnorm writes them (half the
+ * bytes of bf16 where rows travel between the norm and the layer): x_q8 device
+ * e4m3 [n_tokens][hidden], 16-byte aligned, scales device fp32 [n_tokens]
+ * [ceil(hidden / group)], group 32, 64, 128 or >= hidden.  x_bf16 (device bf16
+ * [n_tokens][hidden], 16-byte aligned) receives q * scale, rounded once, and
+ * the result is strata_moe_forward's of it.  Runs on the handle's device, which
+ * must be the current one.  Errors: as strata_moe_forward. */
+strata_status strata_moe_forward_q8(strata_moe *h, const void *x_q8, const float *scales, int group,
+                                    int n_tokens, void *x_bf16, void *out_bf16,
+                                    strata_stream_t stream);
+
 /* ---- Training the router over frozen experts.  The pages describe no
  * training; these calls go with strata_moe_route, whose logits and idx they
  * take.  They keep nothing in the handle but the device status word, run on the
@@ -503,6 +527,7 @@ strata_status strata_moe_balance_backward(strata_moe *h, const float *logits, in
  * terms.  x, dW, dx 16-byte aligned, workspace 256-byte aligned.  Products are
  * taken to fp32 accuracy (dW) or to well below the rounding of bf16 (dx), sums
  * in fp32 in a fixed order.  n_tokens == 0 zeroes dW and db.
+ * dx must not be x.
  * Host errors: INVALID_ARG, CUDA.  Device errors: DEVICE_STATUS (bit 2: an id
  * outside [0, n_experts); that token's dw is ignored, as the forward's output
  * for it is zero). */

@@ -86,6 +86,8 @@ def load_library():
             "strata_moe_balance_backward": (I, [P, P, I, P, I, P, F, P, P, P, P, P]),
             "strata_moe_route_backward_workspace": (Z, [P, I]),
             "strata_moe_route_backward": (I, [P, P, I, P, P, P, P, P, P, P, P, Z, P]),
+            "strata_moe_forward_norm": (I, [P, P, P, P, F, I, P, P, P, P]),
+            "strata_moe_forward_q8": (I, [P, P, P, I, I, P, P, P]),
             "strata_status_str": (ctypes.c_char_p, [I]),
             "strata_arena_create": (I, [P, P, P, ctypes.POINTER(P)]),
             "strata_arena_destroy": (None, [P]),
@@ -113,10 +115,22 @@ def _addr(buf):
     return buf.data_ptr()
 
 
+_torch = None    # torch, imported on first use
+
+
+def _get_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the raw handle of torch.cuda.current_stream() (building the Stream
+        # object alone takes longer than a launch)
+        t = _torch or _get_torch()
+        return t._C._cuda_getCurrentRawStream(t.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -236,13 +250,13 @@ def strata_moe_profile_read(h):
 
 
 DTYPE_BF16, DTYPE_F16, DTYPE_F32 = 0, 1, 2
-_dtypes = None   # torch dtype -> code, filled on first use (torch is imported lazily)
+_dtypes = None   # torch dtype -> code
 
 
 def _dtype(t):
     global _dtypes
     if _dtypes is None:
-        import torch
+        torch = _get_torch()
         _dtypes = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}
     return _dtypes.get(t.dtype, -1)
 
@@ -251,30 +265,42 @@ def _refuse(where):
     raise StrataError(Status.INVALID_ARG, where)
 
 
-def _rows(t, like, where):
-    """(address, row stride) of a 2-D row operand that goes with `like`, or (None, 0)."""
+# Operands of the calls that take torch tensors: their addresses, once their
+# sizes, types and device go together (dev: the device index of the first one).
+def _rows(t, shape, dtype, dev, where):
+    """(address, row stride) of a 2-D operand with unit column stride, or (None, 0)."""
     if t is None:
         return None, 0
-    if (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device
-            or (t.stride(1) != 1 and t.shape[1] > 1)):
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
         _refuse(where)
-    return t.data_ptr(), t.stride(0)
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        _refuse(where)
+    return t.data_ptr(), ld
 
 
-def _flat(t, like, n, itemsize, where):
+def _flat(t, dev, n, itemsize, where):
     """Address of a contiguous operand of n elements of itemsize bytes, or None."""
     if t is None:
         return None
-    if (t.numel() != n or t.element_size() != itemsize or t.device != like.device
+    if (t.numel() != n or t.element_size() != itemsize or t.get_device() != dev
             or not t.is_contiguous()):
         _refuse(where)
     return t.data_ptr()
 
 
-def _on_current(t, where):
+def _workspace(t, dev, where):
+    """(address, bytes) of a workspace, or (None, 0)."""
+    if t is None:
+        return None, 0
+    if t.get_device() != dev or not t.is_contiguous():
+        _refuse(where)
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _on_current(dev, where):
     """A kernel runs on the current device: its operands have to be there."""
-    import torch
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+    if dev < 0 or dev != (_torch or _get_torch()).cuda.current_device():
         _refuse(where)
 
 
@@ -282,23 +308,24 @@ def strata_rmsnorm(x, residual, weight, eps, residual_out=None, out=None, out_q8
                    group=0, stream=None):
     """Rows are torch tensors [tokens][hidden] with unit column stride."""
     w = "strata_rmsnorm"
-    code = _dtype(x)
-    if x.dim() != 2:
+    shape, dt, dev = x.shape, x.dtype, x.get_device()
+    if len(shape) != 2:
         _refuse(w)
-    T, H = x.shape
-    xa, ldx = _rows(x, x, w)
-    ra, ldr = _rows(residual, x, w)
-    roa, ldro = _rows(residual_out, x, w)
-    oa, ldo = _rows(out, x, w)
+    T, H = shape
+    xa, ldx = _rows(x, shape, dt, dev, w)
+    ra, ldr = _rows(residual, shape, dt, dev, w)
+    roa, ldro = _rows(residual_out, shape, dt, dev, w)
+    oa, ldo = _rows(out, shape, dt, dev, w)
     sa = qa = None
     if out_q8 is not None:
         if group <= 0 or scales is None:
             _refuse(w)
-        qa = _flat(out_q8, x, T * H, 1, w)
-        sa = _flat(scales, x, T * -(-H // group), 4, w)
-    _on_current(x, w)
-    _check(_load().strata_rmsnorm(code, xa, ldx, ra, ldr, _flat(weight, x, H, 4, w), eps, T, H, roa,
-                                  ldro, oa, ldo, qa, sa, group, _stream(stream)), w)
+        qa = _flat(out_q8, dev, T * H, 1, w)
+        sa = _flat(scales, dev, T * -(-H // group), 4, w)
+    wa = _flat(weight, dev, H, 4, w)
+    _on_current(dev, w)
+    _check(_load().strata_rmsnorm(_dtype(x), xa, ldx, ra, ldr, wa, eps, T, H, roa, ldro, oa, ldo, qa,
+                                  sa, group, _stream(stream)), w)
 
 
 def strata_rmsnorm_backward_workspace(n_tokens, hidden):
@@ -308,27 +335,31 @@ def strata_rmsnorm_backward_workspace(n_tokens, hidden):
 def strata_rmsnorm_backward(h, weight, eps, dout, dsum, dx, dweight=None, workspace=None,
                             stream=None):
     w = "strata_rmsnorm_backward"
-    code = _dtype(h)
-    if h.dim() != 2:
+    shape, dt, dev = h.shape, h.dtype, h.get_device()
+    if len(shape) != 2:
         _refuse(w)
-    T, H = h.shape
-    ha, ldh = _rows(h, h, w)
-    da, ldd = _rows(dout, h, w)
-    sa, lds = _rows(dsum, h, w)
-    xa, ldx = _rows(dx, h, w)
-    ws, nws = _workspace(workspace, h, w)
-    _on_current(h, w)
-    _check(_load().strata_rmsnorm_backward(code, ha, ldh, _flat(weight, h, H, 4, w), eps, da, ldd,
-                                           sa, lds, T, H, xa, ldx, _flat(dweight, h, H, 4, w), ws,
-                                           nws, _stream(stream)), w)
+    T, H = shape
+    ha, ldh = _rows(h, shape, dt, dev, w)
+    da, ldd = _rows(dout, shape, dt, dev, w)
+    sa, lds = _rows(dsum, shape, dt, dev, w)
+    xa, ldx = _rows(dx, shape, dt, dev, w)
+    wa, dwa = _flat(weight, dev, H, 4, w), _flat(dweight, dev, H, 4, w)
+    ws, nws = _workspace(workspace, dev, w)
+    _on_current(dev, w)
+    _check(_load().strata_rmsnorm_backward(_dtype(h), ha, ldh, wa, eps, da, ldd, sa, lds, T, H, xa,
+                                           ldx, dwa, ws, nws, _stream(stream)), w)
 
 
-def _workspace(t, like, where):
-    if t is None:
-        return None, 0
-    if t.device != like.device or not t.is_contiguous():
-        _refuse(where)
-    return t.data_ptr(), t.numel() * t.element_size()
+def strata_moe_forward_norm(h, x, residual, weight, eps, n_tokens, residual_out, normed, out,
+                            stream=None):
+    _check(_load().strata_moe_forward_norm(h, _addr(x), _addr(residual), _addr(weight), eps,
+                                           n_tokens, _addr(residual_out), _addr(normed),
+                                           _addr(out), _stream(stream)), "strata_moe_forward_norm")
+
+
+def strata_moe_forward_q8(h, x_q8, scales, group, n_tokens, x, out, stream=None):
+    _check(_load().strata_moe_forward_q8(h, _addr(x_q8), _addr(scales), group, n_tokens, _addr(x),
+                                         _addr(out), _stream(stream)), "strata_moe_forward_q8")
 
 
 def strata_moe_balance_workspace(h, n_tokens, n_seq=1):
@@ -489,49 +520,74 @@ class StrataMoE:
     def forward_noalloc(self, x, out, stream=None):
         strata_moe_forward_noalloc(self.h, x, x.shape[0], out, stream)
 
-    # Training the router.  These methods take torch tensors and check that
-    # their sizes go together (StrataError, INVALID_ARG); `workspace` is a
-    # buffer of the size that the *_workspace method gives, kept by the caller.
+    # The calls below take torch tensors and check that their sizes go together
+    # (StrataError, INVALID_ARG).
+    def forward_norm(self, x, residual, weight, eps, residual_out, normed, out, stream=None):
+        w = "strata_moe_forward_norm"
+        T, dev = x.shape[0], x.get_device()
+        n = T * self.hidden
+        a = [_flat(t, dev, n, 2, w) for t in (x, residual, residual_out, normed, out)]
+        wa = _flat(weight, dev, self.hidden, 4, w)
+        _on_current(dev, w)
+        strata_moe_forward_norm(self.h, a[0], a[1], wa, eps, T, a[2], a[3], a[4], stream)
+
+    def forward_q8(self, x_q8, scales, group, x, out, stream=None):
+        w = "strata_moe_forward_q8"
+        T, H, dev = x_q8.shape[0], self.hidden, x_q8.get_device()
+        if group <= 0:
+            _refuse(w)
+        qa, sa = _flat(x_q8, dev, T * H, 1, w), _flat(scales, dev, T * -(-H // group), 4, w)
+        xa, oa = _flat(x, dev, T * H, 2, w), _flat(out, dev, T * H, 2, w)
+        _on_current(dev, w)
+        strata_moe_forward_q8(self.h, qa, sa, group, T, xa, oa, stream)
+
+    # Training the router; `workspace` is a buffer of the size that the
+    # *_workspace method gives, kept by the caller.
     def balance_workspace(self, n_tokens, n_seq=1):
         return strata_moe_balance_workspace(self.h, n_tokens, n_seq)
-
-    def _balance_args(self, logits, counts, tokens, seq_off, mask, where):
-        T, E = logits.shape[0], self.n_experts
-        n_seq = 1 if seq_off is None else seq_off.numel() - 1
-        _on_current(logits, where)
-        return (T, n_seq, _flat(logits, logits, T * E, 4, where),
-                _flat(counts, logits, n_seq * E, 4, where), _flat(tokens, logits, n_seq, 4, where),
-                _flat(seq_off, logits, n_seq + 1, 4, where), _flat(mask, logits, T, 1, where))
 
     def balance(self, logits, idx, coef, counts, tokens, loss, workspace, seq_off=None, mask=None,
                 stream=None):
         w = "strata_moe_balance"
-        T, n_seq, la, ca, ta, sa, ma = self._balance_args(logits, counts, tokens, seq_off, mask, w)
-        ws, nws = _workspace(workspace, logits, w)
-        strata_moe_balance(self.h, la, _flat(idx, logits, T * self.top_k, 4, w), T, coef, ca, ta,
-                           _flat(loss, logits, 1, 4, w), ws, nws, sa, n_seq, ma, stream)
+        T, E, dev = logits.shape[0], self.n_experts, logits.get_device()
+        n_seq = 1 if seq_off is None else seq_off.numel() - 1
+        la, ia = _flat(logits, dev, T * E, 4, w), _flat(idx, dev, T * self.top_k, 4, w)
+        ca, ta = _flat(counts, dev, n_seq * E, 4, w), _flat(tokens, dev, n_seq, 4, w)
+        sa, ma = _flat(seq_off, dev, n_seq + 1, 4, w), _flat(mask, dev, T, 1, w)
+        loa = _flat(loss, dev, 1, 4, w)
+        ws, nws = _workspace(workspace, dev, w)
+        _on_current(dev, w)
+        _check(_load().strata_moe_balance(self.h, la, ia, T, sa, n_seq, ma, coef, ca, ta, loa, ws,
+                                          nws, _stream(stream)), w)
 
     def balance_backward(self, logits, coef, counts, tokens, dlogits, dloss=None, seq_off=None,
                          mask=None, stream=None):
         w = "strata_moe_balance_backward"
-        T, n_seq, la, ca, ta, sa, ma = self._balance_args(logits, counts, tokens, seq_off, mask, w)
-        strata_moe_balance_backward(self.h, la, T, coef, ca, ta,
-                                    _flat(dlogits, logits, T * self.n_experts, 4, w),
-                                    _flat(dloss, logits, 1, 4, w), sa, n_seq, ma, stream)
+        T, E, dev = logits.shape[0], self.n_experts, logits.get_device()
+        n_seq = 1 if seq_off is None else seq_off.numel() - 1
+        la, da = _flat(logits, dev, T * E, 4, w), _flat(dlogits, dev, T * E, 4, w)
+        ca, ta = _flat(counts, dev, n_seq * E, 4, w), _flat(tokens, dev, n_seq, 4, w)
+        sa, ma = _flat(seq_off, dev, n_seq + 1, 4, w), _flat(mask, dev, T, 1, w)
+        dla = _flat(dloss, dev, 1, 4, w)
+        _on_current(dev, w)
+        _check(_load().strata_moe_balance_backward(self.h, la, T, sa, n_seq, ma, coef, ca, ta, dla,
+                                                   da, _stream(stream)), w)
 
     def route_backward_workspace(self, n_tokens):
         return strata_moe_route_backward_workspace(self.h, n_tokens)
 
     def route_backward(self, x, logits, idx, dw, dlogits, dW, db, dx, workspace, stream=None):
         w = "strata_moe_route_backward"
-        T, E, k, H = x.shape[0], self.n_experts, self.top_k, self.hidden
-        _on_current(x, w)
-        ws, nws = _workspace(workspace, x, w)
-        strata_moe_route_backward(self.h, _flat(x, x, T * H, 2, w), T,
-                                  _flat(logits, x, T * E, 4, w), _flat(idx, x, T * k, 4, w),
-                                  _flat(dw, x, T * k, 4, w), _flat(dlogits, x, T * E, 4, w),
-                                  _flat(dW, x, E * H, 4, w), _flat(db, x, E, 4, w),
-                                  _flat(dx, x, T * H, 2, w), ws, nws, stream)
+        T, dev = x.shape[0], x.get_device()
+        E, k, H = self.n_experts, self.top_k, self.hidden
+        xa, dxa = _flat(x, dev, T * H, 2, w), _flat(dx, dev, T * H, 2, w)
+        la, dla = _flat(logits, dev, T * E, 4, w), _flat(dlogits, dev, T * E, 4, w)
+        ia, dwa = _flat(idx, dev, T * k, 4, w), _flat(dw, dev, T * k, 4, w)
+        dWa, dba = _flat(dW, dev, E * H, 4, w), _flat(db, dev, E, 4, w)
+        ws, nws = _workspace(workspace, dev, w)
+        _on_current(dev, w)
+        _check(_load().strata_moe_route_backward(self.h, xa, T, la, ia, dwa, dla, dWa, dba, dxa, ws,
+                                                 nws, _stream(stream)), w)
 
     def status(self, stream=None):
         return strata_moe_get_status(self.h, stream)

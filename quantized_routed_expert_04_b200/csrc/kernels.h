@@ -109,6 +109,10 @@ __global__ void gather_rows_kernel(const __half *x16, const int *pair_tok, const
 size_t tc_smem_bytes();
 int tc_threads();
 
+// ---- e4m3 rows with scales per `group` columns -> bf16 (norm.cu); H % 128 == 0
+cudaError_t run_unpack_q8(const uint8_t *q8, const float *scales, int group, int T, int H,
+                          __nv_bfloat16 *x, cudaStream_t stream);
+
 // ---- balance loss of a batch's routing (balance.cu)
 struct BalanceParams {
   const float *logits;     // [T][E]

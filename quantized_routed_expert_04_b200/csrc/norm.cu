@@ -15,6 +15,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "kernels.h"
 #include "launch.h"
 
 namespace strata {
@@ -451,6 +452,37 @@ cudaError_t launch_norm_grad(const NormGradParams &p, cudaStream_t stream) {
   return launch_pdl(norm_grad_kernel<T, 1024, 16, kVec>, grid, dim3(1024), 0, stream, p);
 }
 
+// ---------------------------------------------------------------- unpack
+// e4m3 rows and their scales -> bf16 activations (the reader of norm_kernel's
+// 8-bit output): 16 elements a thread, always inside one group of scales
+// (groups are multiples of 32; H is a multiple of 128).  The product of the
+// exact e4m3 value and the scale is rounded once to bf16.
+__global__ void __launch_bounds__(256) unpack_q8_kernel(const uint8_t *q8, const float *scales,
+                                                        int group, int n_groups, int H,
+                                                        long long n16, __nv_bfloat16 *x) {
+  grid_dependency_wait();
+  grid_dependency_launch();
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n16) return;
+  const int per_row = H / 16;
+  const long long t = i / per_row;
+  const int c = (int)(i - t * per_row) * 16;
+  const float s = scales[t * n_groups + c / group];
+  const uint4 raw = reinterpret_cast<const uint4 *>(q8)[i];
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((uint16_t)(w[k / 2] >> (16 * (k & 1))), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
+    o[k] = *reinterpret_cast<const uint32_t *>(&b);
+  }
+  uint4 *dst = reinterpret_cast<uint4 *>(x) + 2 * i;
+  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
 int dtype_bytes(int dtype) {
   switch (dtype) {
     case STRATA_DTYPE_BF16: case STRATA_DTYPE_F16: return 2;
@@ -471,6 +503,14 @@ bool rows_vec(const void *p, long long ld, int bytes) {
 }
 
 }  // namespace
+
+cudaError_t run_unpack_q8(const uint8_t *q8, const float *scales, int group, int T, int H,
+                          __nv_bfloat16 *x, cudaStream_t stream) {
+  const long long n16 = (long long)T * H / 16;
+  const int g = group < H ? group : H;
+  return launch_pdl(unpack_q8_kernel, dim3((unsigned)((n16 + 255) / 256)), dim3(256), 0, stream, q8,
+                    scales, g, (H + g - 1) / g, H, n16, x);
+}
 
 }  // namespace strata
 

@@ -677,6 +677,18 @@ strata_status strata_moe_route(strata_moe *h, const void *x_bf16, int n_tokens, 
                     stream);
 }
 
+// What strata_moe_forward refuses.
+static strata_status check_layer_input(const strata_moe *h, const void *x_bf16, int n_tokens,
+                                       const void *out_bf16) {
+  if (!h || n_tokens < 0 || !h->router_W) return STRATA_ERR_INVALID_ARG;
+  for (int i = 0; i < h->S; ++i)
+    if (!h->shared_ptr[i]) return STRATA_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (!x_bf16 || (reinterpret_cast<uintptr_t>(x_bf16) & 15) || !out_bf16 ||
+                       (reinterpret_cast<uintptr_t>(out_bf16) & 15)))
+    return STRATA_ERR_INVALID_ARG;
+  return STRATA_OK;
+}
+
 strata_status strata_moe_forward(strata_moe *h, const void *x_bf16, int n_tokens, void *out_bf16,
                                  strata_stream_t stream) {
   strata_status st = check_common(h, x_bf16, n_tokens, stream);
@@ -708,6 +720,47 @@ strata_status strata_moe_forward_routed(strata_moe *h, const void *x_bf16, int n
   if (st != STRATA_OK) return st;
   if (n_tokens <= kSmallT) return run_fused(h, x_bf16, n_tokens, idx, w, out_bf16, stream);
   return run_experts(h, x_bf16, n_tokens, idx, w, out_bf16, stream);
+}
+
+strata_status strata_moe_forward_norm(strata_moe *h, const void *x_bf16, const void *residual_bf16,
+                                      const float *weight, float eps, int n_tokens,
+                                      void *residual_out_bf16, void *normed_bf16, void *out_bf16,
+                                      strata_stream_t stream) {
+  strata_status st = check_layer_input(h, normed_bf16, n_tokens, out_bf16);
+  if (st != STRATA_OK) return st;
+  int device = -1;
+  if (cudaGetDevice(&device) != cudaSuccess) return STRATA_ERR_CUDA;
+  if (device != h->device) return STRATA_ERR_INVALID_ARG;
+  if (n_tokens == 0) return STRATA_OK;
+  if (out_bf16 == normed_bf16 || out_bf16 == residual_out_bf16) return STRATA_ERR_INVALID_ARG;
+  // before the norm is enqueued, so that a refused call enqueues nothing
+  st = grow_workspace(h, n_tokens);
+  if (st != STRATA_OK) return st;
+  st = strata_rmsnorm(STRATA_DTYPE_BF16, x_bf16, h->H, residual_bf16, h->H, weight, eps, n_tokens,
+                      h->H, residual_out_bf16, h->H, normed_bf16, h->H, nullptr, nullptr, 0, stream);
+  if (st != STRATA_OK) return st;
+  return strata_moe_forward(h, normed_bf16, n_tokens, out_bf16, stream);
+}
+
+strata_status strata_moe_forward_q8(strata_moe *h, const void *x_q8, const float *scales, int group,
+                                    int n_tokens, void *x_bf16, void *out_bf16,
+                                    strata_stream_t stream) {
+  strata_status st = check_layer_input(h, x_bf16, n_tokens, out_bf16);
+  if (st != STRATA_OK) return st;
+  if (group != 32 && group != 64 && group != 128 && group < h->H) return STRATA_ERR_INVALID_ARG;
+  int device = -1;
+  if (cudaGetDevice(&device) != cudaSuccess) return STRATA_ERR_CUDA;
+  if (device != h->device) return STRATA_ERR_INVALID_ARG;
+  if (n_tokens == 0) return STRATA_OK;
+  if (!x_q8 || (reinterpret_cast<uintptr_t>(x_q8) & 15) || !scales ||
+      (reinterpret_cast<uintptr_t>(scales) & 3) || out_bf16 == x_bf16)
+    return STRATA_ERR_INVALID_ARG;
+  st = grow_workspace(h, n_tokens);
+  if (st != STRATA_OK) return st;
+  const cudaError_t e = run_unpack_q8(static_cast<const uint8_t *>(x_q8), scales, group, n_tokens,
+                                      h->H, static_cast<__nv_bfloat16 *>(x_bf16), stream);
+  if (e != cudaSuccess) return cuda_status(e);
+  return strata_moe_forward(h, x_bf16, n_tokens, out_bf16, stream);
 }
 
 strata_status strata_moe_get_status(strata_moe *h, strata_stream_t stream) {
@@ -888,7 +941,8 @@ strata_status strata_moe_route_backward(strata_moe *h, const void *x_bf16, int n
                                         const float *dlogits, float *dW, float *db, void *dx_bf16,
                                         void *workspace, size_t workspace_bytes,
                                         strata_stream_t stream) {
-  if (!h || n_tokens < 0 || n_tokens > kMaxTrainTokens || (!dW && !db && !dx_bf16))
+  if (!h || n_tokens < 0 || n_tokens > kMaxTrainTokens || (!dW && !db && !dx_bf16) ||
+      (dx_bf16 && dx_bf16 == x_bf16))
     return STRATA_ERR_INVALID_ARG;
   if (misaligned(dW, 16) || misaligned(db, 4) || misaligned(dx_bf16, 16)) return STRATA_ERR_INVALID_ARG;
   if (n_tokens > 0) {
