@@ -154,7 +154,12 @@ struct RouteGradParams {
   float *dW, *db;          // [E][H], [E], or null
   __nv_bfloat16 *dx;       // [T][H] or null
   int *status;
-  float *dl;               // set by run_route_grad
+  // set by run_route_grad (workspace)
+  int Epad, tok_blocks;
+  __nv_bfloat16 *dlp;      // [3][T][Epad] bf16 pieces of dl
+  __nv_bfloat16 *Wp;       // [2][E][H] bf16 pieces of W
+  float *db_part;          // [tok_blocks][E]
+  float *dW_part;          // [splits][E][H], or dW itself
 };
 size_t route_grad_workspace(int T, int E, int H);
 cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stream);

@@ -3,7 +3,6 @@
 // sequence of a forward call, the device status word and optional per-kernel
 // timing.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -15,6 +14,7 @@
 #include <vector>
 
 #include "kernels.h"
+#include "launch.h"
 #include "strata_moe.h"
 
 using namespace strata;
@@ -210,19 +210,6 @@ ExpertTable make_table(const strata_moe *h) {
     if (h->slot_expert[s] >= 0) t.ptr[h->slot_expert[s]] = static_cast<const uint8_t *>(h->slot_ptr[s]);
   for (int i = 0; i < h->S; ++i) t.ptr[h->E + i] = static_cast<const uint8_t *>(h->shared_ptr[i]);
   return t;
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    cudaDriverEntryPointQueryResult q;
-    void *ptr = nullptr;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
 }
 
 // Rows of f16 activations [rows][K] as the B operand of the tensor-core
