@@ -14,9 +14,12 @@
 // batches) or by launch latency (small ones).  A row is held by kLanes lanes,
 // 8 consecutive experts each, so a warp works on 32 / kLanes tokens at once
 // and reduces over log2(kLanes) shuffles.  A block takes `chunk` consecutive
-// tokens and walks the pieces of sequences among them; each (block, sequence)
-// piece has a slot of its own, block + sequence, for its partial sums, which
-// the second kernel adds in block order: the result does not depend on timing.
+// tokens and walks the pieces of sequences among them; in the forward, each
+// (block, sequence) piece has a slot of its own, block + sequence, for its
+// partial sums, which the second kernel adds in block order: the result does
+// not depend on timing.
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.h"
@@ -25,9 +28,10 @@ namespace strata {
 
 namespace {
 
-constexpr int kBalThreads = 256;
-constexpr int kBalWarps = kBalThreads / 32;
+constexpr int kSumThreads = 1024;    // forward: one block per multiprocessor
+constexpr int kGradThreads = 256;
 constexpr int kFinishThreads = 1024;
+constexpr int kMaxGridY = 65535;
 
 __device__ __forceinline__ int clamp_int(int v, int lo, int hi) { return min(max(v, lo), hi); }
 
@@ -75,6 +79,18 @@ __device__ __forceinline__ void load_row8(const float *row, int j, int E, bool u
   }
 }
 
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The double at v's place in the shared memory of block `rank` of the cluster.
+__device__ __forceinline__ double cluster_read(const double *v, int rank) {
+  uint32_t at;
+  double d;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(v)), "r"(rank));
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(d) : "r"(at) : "memory");
+  return d;
+}
+
 template <int kLanes>
 __device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
@@ -117,7 +133,7 @@ __device__ __forceinline__ void probabilities(float v[8], bool sigmoid, float sl
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float ex = expf(-v[i]);
-      const float s = __fdiv_rn(1.0f, 1.0f + ex);
+      const float s = __fdividef(1.0f, 1.0f + ex);   // within 1 unit, 0 beyond 2^126
       // s (1 - s) with 1 - s = ex s, or 1 where ex is beyond fp32 (s = 0)
       if (kSlope) slope[i] = s == 0.0f ? 0.0f : s * (ex * s);
       v[i] = s;
@@ -133,65 +149,112 @@ __device__ __forceinline__ void probabilities(float v[8], bool sigmoid, float sl
   }
 }
 
+// The block's share of one sequence's tokens [a, e): sums of p per expert into
+// s_p[0], counts into s_cnt, counted tokens into s_tok.
 template <int kLanes, bool kVec>
-__global__ void __launch_bounds__(kBalThreads) balance_partial_kernel(const BalanceParams p) {
-  __shared__ float s_p[kBalWarps][kLanes * 8];
+__device__ __forceinline__ void sum_piece(const BalanceParams &p, int a, int e, float (*s_p)[kLanes * 8],
+                                          int *s_cnt, int *s_tok) {
+  constexpr int kTok = 32 / kLanes;   // tokens a warp works on at once
+  constexpr int kWarps = kSumThreads / 32;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int j = lane % kLanes, sub = lane / kLanes;
+  const int E = p.E, k = p.k;
+  for (int i = tid; i < E; i += kSumThreads) s_cnt[i] = 0;
+  if (tid == 0) *s_tok = 0;
+  __syncthreads();
+  float acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+  int n = 0;
+  auto counted = [&](int tok) { return tok < e && (!p.mask || p.mask[tok] != 0); };
+  // the next token's row is loaded before this one's is reduced
+  float next[8];
+  bool next_live = counted(a + warp * kTok + sub);
+  load_row8<kVec>(p.logits + (size_t)(a + warp * kTok + sub) * E, j, E, next_live, next);
+  for (int t0 = a + warp * kTok; t0 < e; t0 += kWarps * kTok) {
+    const int tok = t0 + sub;
+    const bool live = next_live;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = next[i];
+    const int ahead = tok + kWarps * kTok;
+    next_live = counted(ahead);
+    load_row8<kVec>(p.logits + (size_t)ahead * E, j, E, next_live, next);
+    if (live) {   // counts: integers, in any order
+      for (int i = j; i < k; i += kLanes) {
+        const int id = p.idx[(size_t)tok * k + i];
+        if (id < 0 || id >= E)
+          set_status(p.status, STATUS_BAD_ROUTING);
+        else
+          atomicAdd(&s_cnt[id], 1);
+      }
+    }
+    __syncwarp();
+    probabilities<kLanes, false>(v, p.sigmoid, nullptr);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] += live ? v[i] : 0.0f;
+    n += live && j == 0;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int o = kLanes; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    if (sub == 0) s_p[warp][8 * j + i] = acc[i];
+  }
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0 && n) atomicAdd(s_tok, n);
+  __syncthreads();
+  for (int i = tid; i < E; i += kSumThreads) {
+    float s = s_p[0][i];
+#pragma unroll 8
+    for (int w = 1; w < kWarps; ++w) s += s_p[w][i];
+    s_p[0][i] = s;
+  }
+}
+
+// kWhole: one block takes the whole batch, one sequence, and writes the
+// results itself.
+template <int kLanes, bool kVec, bool kWhole>
+__global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceParams p) {
+  __shared__ float s_p[kSumThreads / 32][kLanes * 8];
   __shared__ int s_cnt[kLanes * 8];
   __shared__ int s_tok;
   grid_dependency_wait();
   grid_dependency_launch();
-  constexpr int kTok = 32 / kLanes;   // tokens a warp works on at once
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int j = lane % kLanes, sub = lane / kLanes;
-  const int E = p.E, k = p.k;
+  const int tid = threadIdx.x, E = p.E;
+  if (kWhole) {
+    const Span sp = seq_span(p, 0);
+    if (p.seq_off && tid == 0 && (p.seq_off[0] != sp.a || p.seq_off[1] != sp.e))
+      set_status(p.status, STATUS_BOUNDS);
+    sum_piece<kLanes, kVec>(p, sp.a, sp.e, s_p, s_cnt, &s_tok);
+    __syncthreads();
+    if (tid < 32) {
+      const int nb = s_tok;
+      double all = 0.0;
+      for (int i = tid; i < E; i += 32) {
+        p.counts[i] = s_cnt[i];
+        if (nb > 0) all += (double)s_cnt[i] * E / ((double)p.k * nb) * ((double)s_p[0][i] / nb);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+      if (tid == 0) {
+        p.tokens[0] = nb;
+        p.loss[0] = (float)((double)p.coef * all);
+      }
+    }
+    return;
+  }
   int t = blockIdx.x * p.chunk;
   const int t_end = min(p.T, t + p.chunk);
   for (int b = first_seq(p, t); b < p.n_seq && t < t_end; ++b) {
     const Span sp = seq_span(p, b);
     const int a = max(sp.a, t), e = min(sp.e, t_end);
     if (a >= e) continue;
-    for (int i = tid; i < E; i += kBalThreads) s_cnt[i] = 0;
-    if (tid == 0) s_tok = 0;
-    __syncthreads();
-    float acc[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
-    int n = 0;
-    for (int t0 = a + warp * kTok; t0 < e; t0 += kBalWarps * kTok) {
-      const int tok = t0 + sub;
-      const bool live = tok < e && (!p.mask || p.mask[tok] != 0);
-      float v[8];
-      load_row8<kVec>(p.logits + (size_t)tok * E, j, E, live, v);
-      probabilities<kLanes, false>(v, p.sigmoid, nullptr);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += live ? v[i] : 0.0f;
-      n += live && j == 0;
-    }
-    // counts: one pair a thread, added up in shared memory (integers: any order)
-    const long long q1 = (long long)e * k;
-    for (long long q = (long long)a * k + tid; q < q1; q += kBalThreads) {
-      if (p.mask && !p.mask[q / k]) continue;
-      const int id = p.idx[q];
-      if (id < 0 || id >= E)
-        set_status(p.status, STATUS_BAD_ROUTING);
-      else
-        atomicAdd(&s_cnt[id], 1);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-#pragma unroll
-      for (int o = kLanes; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-      if (sub == 0) s_p[warp][8 * j + i] = acc[i];
-    }
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0 && n) atomicAdd(&s_tok, n);
-    __syncthreads();
+    sum_piece<kLanes, kVec>(p, a, e, s_p, s_cnt, &s_tok);
+    // (each thread wrote the s_p[0] that it reads here)
     const size_t slot = (size_t)blockIdx.x + b;
-    for (int i = tid; i < E; i += kBalThreads) {
-      float s = s_p[0][i];
-#pragma unroll
-      for (int w = 1; w < kBalWarps; ++w) s += s_p[w][i];
-      p.part_p[slot * E + i] = s;
+    for (int i = tid; i < E; i += kSumThreads) {
+      p.part_p[slot * E + i] = s_p[0][i];
       p.part_cnt[slot * E + i] = s_cnt[i];
     }
     if (tid == 0) p.part_tok[slot] = s_tok;
@@ -200,15 +263,17 @@ __global__ void __launch_bounds__(kBalThreads) balance_partial_kernel(const Bala
   }
 }
 
-// One block per sequence: adds its pieces' slots, writes its counts and its
-// sum of f P.
+// A cluster of blocks per sequence, 32 experts a block: adds the slots of the
+// sequence's pieces, writes its counts; the first block adds up the sum of
+// f P over the cluster.
 __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(const BalanceParams p) {
-  __shared__ double s_p[kFinishThreads];
-  __shared__ int s_c[kFinishThreads];
+  __shared__ double s_p[32][33];
+  __shared__ int s_c[32][33];
   __shared__ int s_tok;
+  __shared__ double s_term;
   grid_dependency_wait();
   grid_dependency_launch();
-  const int b = blockIdx.x, tid = threadIdx.x, E = p.E;
+  const int b = p.seq0 + blockIdx.y, tid = threadIdx.x, E = p.E;
   const Span sp = seq_span(p, b);
   if (p.seq_off && tid == 0 && (p.seq_off[b] != sp.a || p.seq_off[b + 1] != sp.e))
     set_status(p.status, STATUS_BOUNDS);
@@ -216,45 +281,55 @@ __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(const Ba
   const int n = sp.e > sp.a ? (sp.e - 1) / p.chunk - c0 + 1 : 0;
   if (tid == 0) s_tok = 0;
   __syncthreads();
-  const int x = tid % kMaxExperts, y = tid / kMaxExperts;   // expert, share of the slots
-  constexpr int kShares = kFinishThreads / kMaxExperts;
+  const int lane = tid & 31, y = tid >> 5;   // expert of the block, share of the slots
+  const int x = blockIdx.x * 32 + lane;
   double sum = 0.0;
   int cnt = 0, tok = 0;
   for (int i = tid; i < n; i += kFinishThreads) tok += p.part_tok[c0 + i + b];
-  if (x < E)
-    for (int i = y; i < n; i += kShares) {
+  if (x < E) {
+#pragma unroll 5
+    for (int i = y; i < n; i += 32) {
       const size_t slot = (size_t)c0 + i + b;
       sum += (double)p.part_p[slot * E + x];
       cnt += p.part_cnt[slot * E + x];
     }
+  }
   tok = __reduce_add_sync(0xffffffffu, tok);
-  if ((tid & 31) == 0 && tok) atomicAdd(&s_tok, tok);
-  s_p[tid] = sum;
-  s_c[tid] = cnt;
+  if (lane == 0 && tok) atomicAdd(&s_tok, tok);
+  s_p[y][lane] = sum;
+  s_c[y][lane] = cnt;
   __syncthreads();
   const int nb = s_tok;
-  double term = 0.0;
-  if (y == 0 && x < E) {
-    for (int i = 1; i < kShares; ++i) {
-      sum += s_p[i * kMaxExperts + x];
-      cnt += s_c[i * kMaxExperts + x];
-    }
-    p.counts[(size_t)b * E + x] = cnt;
-    if (nb > 0) term = (double)cnt * E / ((double)p.k * nb) * (sum / nb);
+  // warp y: the 32 shares of expert 32 blockIdx.x + y
+  sum = s_p[lane][y];
+  cnt = s_c[lane][y];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  cnt = __reduce_add_sync(0xffffffffu, cnt);
+  const int xe = blockIdx.x * 32 + y;
+  __syncthreads();
+  if (lane == 0) {
+    if (xe < E) p.counts[(size_t)b * E + xe] = cnt;
+    s_p[0][y] = xe < E && nb > 0 ? (double)cnt * E / ((double)p.k * nb) * (sum / nb) : 0.0;
   }
   __syncthreads();
-  for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
-  if ((tid & 31) == 0) s_p[tid >> 5] = term;
-  __syncthreads();
-  if (tid == 0) {
+  if (y == 0) {
+    double term = s_p[0][lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
+    if (lane == 0) s_term = term;
+  }
+  cluster_sync();
+  if (blockIdx.x == 0 && tid == 0) {
     double all = 0.0;
-    for (int w = 0; w < kMaxExperts / 32; ++w) all += s_p[w];
+    for (int r = 0; r < (int)gridDim.x; ++r) all += cluster_read(&s_term, r);
     p.tokens[b] = nb;
     if (p.n_seq == 1)
       p.loss[0] = (float)((double)p.coef * all);
     else
       p.seq_loss[b] = all;
   }
+  cluster_sync();   // no block leaves while its s_term may still be read
 }
 
 // The mean of the sequences' sums, in a fixed order.
@@ -274,7 +349,7 @@ __global__ void __launch_bounds__(256) balance_mean_kernel(const BalanceParams p
 }
 
 template <int kLanes, bool kVec>
-__global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const BalanceGradParams g) {
+__global__ void __launch_bounds__(kGradThreads) balance_grad_kernel(const BalanceGradParams g) {
   grid_dependency_wait();
   grid_dependency_launch();
   const BalanceParams &p = g.p;
@@ -287,12 +362,24 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const Balance
   const float dloss = g.dloss ? *g.dloss : 1.0f;
   // tokens [a, e) with the weights f and the factor u (zeros if !counted)
   auto piece = [&](int a, int e, bool counted, const float f[8], float u) {
-    for (int t0 = a + warp * kTok; t0 < e; t0 += kBalWarps * kTok) {
-      const int tok = t0 + sub;
-      const bool in = tok < e;
-      const bool live = counted && in && (!p.mask || p.mask[tok] != 0);
+    // last token first: the forward's last rows are still in L2, where the
+    // batch as a whole does not fit; the next row is loaded ahead
+    constexpr int kStep = kGradThreads / 32 * kTok;
+    auto used = [&](int tok) {
+      return counted && tok >= a && (!p.mask || p.mask[tok] != 0);
+    };
+    int tok = e - 1 - warp * kTok - sub;
+    float next[8];
+    bool next_live = used(tok);
+    load_row8<kVec>(p.logits + (long long)tok * E, j, E, next_live, next);
+    for (int t1 = e - 1 - warp * kTok; t1 >= a; t1 -= kStep, tok -= kStep) {
+      const bool in = tok >= a;
+      const bool live = next_live;
       float v[8], slope[8];
-      load_row8<kVec>(p.logits + (size_t)tok * E, j, E, live, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = next[i];
+      next_live = used(tok - kStep);
+      load_row8<kVec>(p.logits + ((long long)tok - kStep) * E, j, E, next_live, next);
       probabilities<kLanes, true>(v, p.sigmoid, slope);
       float dot = 0.0f;
 #pragma unroll
@@ -300,7 +387,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const Balance
       dot = lanes_sum<kLanes>(dot);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = live ? u * slope[i] * (f[i] - dot) : 0.0f;
-      float *out = g.dlogits + (size_t)tok * E + 8 * j;
+      float *out = g.dlogits + (long long)tok * E + 8 * j;
       if (kVec) {
         if (in && 8 * j < E) {
           reinterpret_cast<float4 *>(out)[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -334,13 +421,21 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const Balance
   piece(t, t_end, false, f, 0.0f);   // tokens behind the last sequence
 }
 
-// Tokens per block: a multiple of 8 that gives the 148 multiprocessors up to
-// four blocks each.
-int balance_chunk(int T) {
+// Forward: tokens per block, a multiple of 32, that give each of the 148
+// multiprocessors one block of 32 warps.
+int sum_chunk(int T) { return std::max(32, ((T + 147) / 148 + 31) & ~31); }
+int sum_blocks(int T) { return (T + sum_chunk(T) - 1) / sum_chunk(T); }
+// Backward: up to four blocks of 8 warps each, at least two rows a warp.
+int grad_chunk(int T) {
   const int per = (T + 591) / 592;
   return ((per < 16 ? 16 : per) + 7) & ~7;
 }
-int balance_blocks(int T) { return (int)(((long long)T + balance_chunk(T) - 1) / balance_chunk(T)); }
+// Batches that one block passes over in at most four steps take one launch.
+bool whole_batch(const BalanceParams &p) {
+  int lanes = 1;
+  while (8 * lanes < p.E) lanes *= 2;
+  return p.n_seq == 1 && p.T <= 4 * (kSumThreads / lanes);
+}
 
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -360,17 +455,20 @@ cudaError_t by_shape(int E, bool vec, A... a) {
 }
 
 template <int kLanes, bool kVec>
-struct LaunchPartial {
-  static cudaError_t run(const BalanceParams *p, cudaStream_t stream) {
-    return launch_pdl(balance_partial_kernel<kLanes, kVec>, dim3(balance_blocks(p->T)),
-                      dim3(kBalThreads), 0, stream, *p);
+struct LaunchSum {
+  static cudaError_t run(const BalanceParams *p, bool whole, cudaStream_t stream) {
+    if (whole)
+      return launch_pdl(balance_sum_kernel<kLanes, kVec, true>, dim3(1), dim3(kSumThreads), 0, stream, *p);
+    return launch_pdl(balance_sum_kernel<kLanes, kVec, false>, dim3(sum_blocks(p->T)),
+                      dim3(kSumThreads), 0, stream, *p);
   }
 };
 template <int kLanes, bool kVec>
 struct LaunchGrad {
   static cudaError_t run(const BalanceGradParams *g, cudaStream_t stream) {
-    return launch_pdl(balance_grad_kernel<kLanes, kVec>, dim3(balance_blocks(g->p.T)),
-                      dim3(kBalThreads), 0, stream, *g);
+    const int chunk = g->p.chunk;
+    return launch_pdl(balance_grad_kernel<kLanes, kVec>, dim3((g->p.T + chunk - 1) / chunk),
+                      dim3(kGradThreads), 0, stream, *g);
   }
 };
 
@@ -381,28 +479,35 @@ inline bool vec_rows(const void *p, int E) {
 }  // namespace
 
 size_t balance_workspace(int T, int E, int n_seq) {
-  const size_t slots = (size_t)balance_blocks(T) + n_seq;
+  const size_t slots = (size_t)sum_blocks(T) + n_seq;
   return 2 * up256(slots * E * 4) + up256(slots * 4) + up256((size_t)n_seq * 8);
 }
 
 cudaError_t run_balance(BalanceParams p, void *workspace, cudaStream_t stream) {
-  const size_t slots = (size_t)balance_blocks(p.T) + p.n_seq;
+  const size_t slots = (size_t)sum_blocks(p.T) + p.n_seq;
   char *w = static_cast<char *>(workspace);
   p.part_p = reinterpret_cast<float *>(w);
   p.part_cnt = reinterpret_cast<int *>(w += up256(slots * p.E * 4));
   p.part_tok = reinterpret_cast<int *>(w += up256(slots * p.E * 4));
   p.seq_loss = reinterpret_cast<double *>(w += up256(slots * 4));
-  p.chunk = balance_chunk(p.T);
-  cudaError_t e = by_shape<LaunchPartial>(p.E, vec_rows(p.logits, p.E), (const BalanceParams *)&p, stream);
-  if (e == cudaSuccess)
-    e = launch_pdl(balance_finish_kernel, dim3(p.n_seq), dim3(kFinishThreads), 0, stream, p);
+  p.chunk = sum_chunk(p.T);
+  const bool whole = whole_batch(p);
+  cudaError_t e =
+      by_shape<LaunchSum>(p.E, vec_rows(p.logits, p.E), (const BalanceParams *)&p, whole, stream);
+  if (whole || e != cudaSuccess) return e;
+  for (int b0 = 0; e == cudaSuccess && b0 < p.n_seq; b0 += kMaxGridY) {
+    p.seq0 = b0;
+    const int groups = (p.E + 31) / 32;
+    e = launch_pdl_cluster(balance_finish_kernel, dim3(groups, std::min(p.n_seq - b0, kMaxGridY)),
+                           groups, dim3(kFinishThreads), 0, stream, p);
+  }
   if (e == cudaSuccess && p.n_seq > 1)
     e = launch_pdl(balance_mean_kernel, dim3(1), dim3(256), 0, stream, p);
   return e;
 }
 
 cudaError_t run_balance_grad(BalanceGradParams g, cudaStream_t stream) {
-  g.p.chunk = balance_chunk(g.p.T);
+  g.p.chunk = grad_chunk(g.p.T);
   const bool vec = vec_rows(g.p.logits, g.p.E) && vec_rows(g.dlogits, g.p.E);
   return by_shape<LaunchGrad>(g.p.E, vec, (const BalanceGradParams *)&g, stream);
 }

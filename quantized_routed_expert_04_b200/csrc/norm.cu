@@ -324,132 +324,159 @@ struct NormGradParams {
 };
 
 // One block walks rows blockIdx.x, + gridDim.x, ...; a thread keeps its
-// columns' weight-gradient sums in registers over all of them.
-template <typename T, int kTpr, int kNe, bool kVec>
-__global__ void __launch_bounds__(kTpr) norm_grad_kernel(const NormGradParams p) {
-  __shared__ float s_red[2][2][kTpr / 32];
+// columns' weights and weight-gradient sums in registers over all of them.
+// With kVec the next row's loads are issued before the current row is reduced,
+// so that memory is never idle through a reduction.
+template <typename T, int kTpr, int kNe, bool kVec, int kMinBlocks>
+__global__ void __launch_bounds__(kTpr, kMinBlocks) norm_grad_kernel(const NormGradParams p) {
+  constexpr int kWarps = kTpr / 32, kNv = kVec ? kNe / 8 : 1;
+  __shared__ float2 s_red[2][kWarps];
   grid_dependency_wait();
   grid_dependency_launch();
   const int tid = threadIdx.x, H = p.H;
   auto col = [&](int i) { return kVec ? (tid + (i / 8) * kTpr) * 8 + i % 8 : tid + i * kTpr; };
-  float dg[kNe];
+  float dg[kNe], w[kNe];
 #pragma unroll
-  for (int i = 0; i < kNe; ++i) dg[i] = 0.0f;
-  int flip = 0;
-  for (long long row = blockIdx.x; row < p.T; row += gridDim.x, flip ^= 1) {
+  for (int i = 0; i < kNe; ++i) {
+    dg[i] = 0.0f;
+    w[i] = col(i) < H ? __ldg(p.weight + col(i)) : 0.0f;
+  }
+  Vec8<T> hn[kNv], dn[kNv], sn[kNv];   // the next row
+  const bool direct = p.dsum != nullptr;
+  auto fetch = [&](long long row) {
+    if (!kVec || row >= p.T) return;
     const T *h = static_cast<const T *>(p.h) + row * p.ldh;
     const T *dy = static_cast<const T *>(p.dout) + row * p.lddo;
-    const T *ds = p.dsum ? static_cast<const T *>(p.dsum) + row * p.ldds : nullptr;
-    T *dx = static_cast<T *>(p.dx) + row * p.lddx;
-    float a[kNe], d[kNe];
-    if (kVec) {
+    const T *ds = static_cast<const T *>(p.dsum) + row * p.ldds;
 #pragma unroll
-      for (int i = 0; i < kNe; i += 8) {
-        const int c = col(i);
-        Vec8<T> ha, da;
-        if (c < H) {
-          ha = load8(h + c);
-          da = load8(dy + c);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          a[i + j] = c < H ? to_f32(ha.v[j]) : 0.0f;
-          d[i + j] = c < H ? to_f32(da.v[j]) : 0.0f;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kNe; ++i) {
-        const int c = col(i);
-        a[i] = c < H ? to_f32(h[c]) : 0.0f;
-        d[i] = c < H ? to_f32(dy[c]) : 0.0f;
+    for (int i = 0; i < kNv; ++i) {
+      const int c = col(8 * i);
+      if (c < H) {
+        hn[i] = load8(h + c);
+        dn[i] = load8(dy + c);
+        if (direct) sn[i] = load8(ds + c);
       }
     }
+  };
+  fetch(blockIdx.x);
+  int flip = 0;
+  for (long long row = blockIdx.x; row < p.T; row += gridDim.x, flip ^= 1) {
+    float a[kNe], d[kNe];
+    Vec8<T> sc[kNv];
+    if (kVec) {
+#pragma unroll
+      for (int i = 0; i < kNe; ++i) {
+        const bool in = col(i - i % 8) < H;
+        a[i] = in ? to_f32(hn[i / 8].v[i % 8]) : 0.0f;
+        d[i] = in ? to_f32(dn[i / 8].v[i % 8]) : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < kNv; ++i) sc[i] = sn[i];
+      fetch(row + gridDim.x);
+    } else {
+      const T *h = static_cast<const T *>(p.h) + row * p.ldh;
+      const T *dy = static_cast<const T *>(p.dout) + row * p.lddo;
+#pragma unroll
+      for (int i = 0; i < kNe; ++i) a[i] = col(i) < H ? to_f32(h[col(i)]) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < kNe; ++i) d[i] = col(i) < H ? to_f32(dy[col(i)]) : 0.0f;
+    }
     float sq = 0.0f, dot = 0.0f;
-    float w[kNe];
 #pragma unroll
     for (int i = 0; i < kNe; ++i) {
-      const int c = col(i);
-      w[i] = c < H ? __ldg(p.weight + c) : 0.0f;
       sq = fmaf(a[i], a[i], sq);
       dot = fmaf(d[i] * w[i], a[i], dot);
     }
-    sq = row_reduce<kTpr>(sq, SumOp(), s_red[flip][0], tid);
-    dot = row_reduce<kTpr>(dot, SumOp(), s_red[flip][1], tid);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      sq += __shfl_xor_sync(0xffffffffu, sq, o);
+      dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    }
+    if (kWarps > 1) {
+      // (two slots in turn: a warp is at most one row ahead of the others)
+      if ((tid & 31) == 0) s_red[flip][tid >> 5] = make_float2(sq, dot);
+      __syncthreads();
+      const float2 v = s_red[flip][tid & (kWarps - 1)];
+      sq = v.x;
+      dot = v.y;
+#pragma unroll
+      for (int o = kWarps / 2; o > 0; o >>= 1) {
+        sq += __shfl_xor_sync(0xffffffffu, sq, o);
+        dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      }
+    }
     const float inv = __fdiv_rn(1.0f, __fsqrt_rn(sq / (float)H + p.eps));
     const float back = dot * inv * inv / (float)H;   // i^2 mean(gy h)
-    float o[kNe];
+    T *dx = static_cast<T *>(p.dx) + row * p.lddx;
+    const T *ds = static_cast<const T *>(p.dsum) + row * p.ldds;
+    Vec8<T> e[kNv];
 #pragma unroll
     for (int i = 0; i < kNe; ++i) {
       dg[i] = fmaf(d[i], a[i] * inv, dg[i]);
-      o[i] = inv * (d[i] * w[i] - a[i] * back);
+      float o = inv * (d[i] * w[i] - a[i] * back);
+      if (kVec) {
+        if (direct) o += to_f32(sc[i / 8].v[i % 8]);
+        e[i / 8].v[i % 8] = from_f32<T>(o);
+      } else if (col(i) < H) {
+        dx[col(i)] = from_f32<T>(direct ? o + to_f32(ds[col(i)]) : o);
+      }
     }
     if (kVec) {
 #pragma unroll
-      for (int i = 0; i < kNe; i += 8) {
-        const int c = col(i);
-        if (c < H) {
-          Vec8<T> e, s;
-          if (ds) s = load8(ds + c);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            e.v[j] = from_f32<T>(ds ? o[i + j] + to_f32(s.v[j]) : o[i + j]);
-          store8(dx + c, e);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kNe; ++i) {
-        const int c = col(i);
-        if (c < H) dx[c] = from_f32<T>(ds ? o[i] + to_f32(ds[c]) : o[i]);
-      }
+      for (int i = 0; i < kNv; ++i)
+        if (col(8 * i) < H) store8(dx + col(8 * i), e[i]);
     }
   }
   if (p.partial) {
     float *out = p.partial + (long long)blockIdx.x * H;
 #pragma unroll
-    for (int i = 0; i < kNe; ++i) {
-      const int c = col(i);
-      if (c < H) out[c] = dg[i];
-    }
+    for (int i = 0; i < kNe; ++i)
+      if (col(i) < H) out[col(i)] = dg[i];
   }
 }
 
-// Sum of n rows of partial sums, in a fixed order: 32 columns a block, 8 row
-// lanes.
-__global__ void __launch_bounds__(256) norm_grad_sum_kernel(const float *partial, int n, int H,
-                                                            float *out) {
-  __shared__ float s[8][33];
+// Sum of n <= 296 rows of partial sums, in a fixed order: 32 columns a block,
+// 32 rows at a time.
+__global__ void __launch_bounds__(1024) norm_grad_sum_kernel(const float *partial, int n, int H,
+                                                             float *out) {
+  __shared__ float s[32][33];
   grid_dependency_wait();
   grid_dependency_launch();
   const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.0f;
-  if (c < H)
-    for (int r = y; r < n; r += 8) v += partial[(long long)r * H + c];
+  if (c < H) {
+#pragma unroll 10
+    for (int r = y; r < n; r += 32) v += partial[(long long)r * H + c];
+  }
   s[y][lane] = v;
   __syncthreads();
-  if (y == 0 && c < H) {
+  v = s[lane][y];   // row share lane of column y
 #pragma unroll
-    for (int i = 1; i < 8; ++i) v += s[i][lane];
-    out[c] = v;
-  }
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int cy = blockIdx.x * 32 + y;
+  if (lane == 0 && cy < H) out[cy] = v;
 }
 
-// Blocks of the gradient kernel: enough for every multiprocessor (148) twice
-// at the most.
-constexpr int kGradBlocks = 296;
-inline int grad_blocks(int T) { return T < kGradBlocks ? T : kGradBlocks; }
+// Blocks of the gradient kernel: two for each of the 148 multiprocessors, half
+// as many where that leaves a block fewer than four rows (each block's partial
+// sums are as long as a row and are read again).
+inline int grad_blocks(int T) { return T >= 1184 ? 296 : T < 148 ? T : 148; }
 
 template <typename T, bool kVec>
 cudaError_t launch_norm_grad(const NormGradParams &p, cudaStream_t stream) {
   const dim3 grid(grad_blocks(p.T));
-  if (p.H <= 512) return launch_pdl(norm_grad_kernel<T, 64, 8, kVec>, grid, dim3(64), 0, stream, p);
-  if (p.H <= 1024) return launch_pdl(norm_grad_kernel<T, 128, 8, kVec>, grid, dim3(128), 0, stream, p);
-  if (p.H <= 2048) return launch_pdl(norm_grad_kernel<T, 256, 8, kVec>, grid, dim3(256), 0, stream, p);
-  if (p.H <= 4096) return launch_pdl(norm_grad_kernel<T, 512, 8, kVec>, grid, dim3(512), 0, stream, p);
-  if (p.H <= 8192) return launch_pdl(norm_grad_kernel<T, 1024, 8, kVec>, grid, dim3(1024), 0, stream, p);
-  return launch_pdl(norm_grad_kernel<T, 1024, 16, kVec>, grid, dim3(1024), 0, stream, p);
+  if (p.H <= 256) return launch_pdl(norm_grad_kernel<T, 32, 8, kVec, 2>, grid, dim3(32), 0, stream, p);
+  if (p.H <= 512) return launch_pdl(norm_grad_kernel<T, 64, 8, kVec, 2>, grid, dim3(64), 0, stream, p);
+  if (p.H <= 1024) return launch_pdl(norm_grad_kernel<T, 128, 8, kVec, 2>, grid, dim3(128), 0, stream, p);
+  if (p.H <= 2048) return launch_pdl(norm_grad_kernel<T, 256, 8, kVec, 2>, grid, dim3(256), 0, stream, p);
+  if (p.H <= 4096) {
+    if (sizeof(T) == 2)
+      return launch_pdl(norm_grad_kernel<T, 256, 16, kVec, 2>, grid, dim3(256), 0, stream, p);
+    return launch_pdl(norm_grad_kernel<T, 512, 8, kVec, 1>, grid, dim3(512), 0, stream, p);
+  }
+  if (p.H <= 8192) return launch_pdl(norm_grad_kernel<T, 512, 16, kVec, 1>, grid, dim3(512), 0, stream, p);
+  return launch_pdl(norm_grad_kernel<T, 1024, 16, kVec, 1>, grid, dim3(1024), 0, stream, p);
 }
 
 // ---------------------------------------------------------------- unpack
@@ -629,7 +656,7 @@ strata_status strata_rmsnorm_backward(int dtype, const void *h, long long h_stri
       e = vec ? launch_norm_grad<float, true>(p, stream) : launch_norm_grad<float, false>(p, stream);
   }
   if (e == cudaSuccess && dweight)
-    e = launch_pdl(norm_grad_sum_kernel, dim3((hidden + 31) / 32), dim3(256), 0, stream,
+    e = launch_pdl(norm_grad_sum_kernel, dim3((hidden + 31) / 32), dim3(1024), 0, stream,
                    (const float *)p.partial, grad_blocks(n_tokens), hidden, dweight);
   return status_of(e);
 }
