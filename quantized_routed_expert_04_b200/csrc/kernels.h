@@ -160,7 +160,7 @@ struct RouteGradParams {
   __nv_bfloat16 *dlp;      // [3][T][Epad] bf16 pieces of dl
   __nv_bfloat16 *Wp;       // [2][E][H] bf16 pieces of W
   float *db_part;          // [tok_blocks][E]
-  float *dW_part;          // [splits][E][H], or dW itself
+  float *dW_part;          // parts of dW, [slot][E][256]
 };
 size_t route_grad_workspace(int T, int E, int H);
 cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stream);

@@ -14,6 +14,8 @@
 // elements one by one, which keeps every access of a warp contiguous.
 #include <cuda_fp8.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.h"
@@ -23,6 +25,7 @@ namespace strata {
 namespace {
 
 constexpr int kNormMaxH = 16384;
+constexpr int kMaxStages = 8;
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T v);
@@ -44,8 +47,8 @@ __device__ __forceinline__ float from_f32(float v) { return v; }
 
 // Eight elements as they are stored.
 template <typename T>
-struct alignas(16) Vec8 {
-  T v[8];
+struct Vec8 {
+  uint4 q[sizeof(T) / 2];
 };
 
 // Plain loads and stores (never the read-only path: an output may be the same
@@ -53,18 +56,62 @@ struct alignas(16) Vec8 {
 template <typename T>
 __device__ __forceinline__ Vec8<T> load8(const T *p) {
   Vec8<T> r;
-  uint4 *d = reinterpret_cast<uint4 *>(&r);
-  const uint4 *s = reinterpret_cast<const uint4 *>(p);
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(Vec8<T>) / 16; ++i) d[i] = s[i];
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.q[i] = reinterpret_cast<const uint4 *>(p)[i];
   return r;
 }
 template <typename T>
 __device__ __forceinline__ void store8(T *p, const Vec8<T> &r) {
-  const uint4 *s = reinterpret_cast<const uint4 *>(&r);
-  uint4 *d = reinterpret_cast<uint4 *>(p);
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(Vec8<T>) / 16; ++i) d[i] = s[i];
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4 *>(p)[i] = r.q[i];
+}
+
+__device__ __forceinline__ float2 unpack2(uint32_t w, __nv_bfloat16) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w, __half) { return __half22float2(bits_h2(w)); }
+__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
+  return h2_bits(__floats2half2_rn(a, b));
+}
+template <typename T>
+__device__ __forceinline__ void unpack8(const Vec8<T> &r, float v[8]) {
+  const uint32_t w[4] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack2(w[i], T());
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+template <>
+__device__ __forceinline__ void unpack8(const Vec8<float> &r, float v[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v[4 * i] = __uint_as_float(r.q[i].x);
+    v[4 * i + 1] = __uint_as_float(r.q[i].y);
+    v[4 * i + 2] = __uint_as_float(r.q[i].z);
+    v[4 * i + 3] = __uint_as_float(r.q[i].w);
+  }
+}
+template <typename T>
+__device__ __forceinline__ Vec8<T> pack8(const float v[8]) {
+  Vec8<T> r;
+  r.q[0] = make_uint4(pack2(v[0], v[1], T()), pack2(v[2], v[3], T()), pack2(v[4], v[5], T()),
+                      pack2(v[6], v[7], T()));
+  return r;
+}
+template <>
+__device__ __forceinline__ Vec8<float> pack8<float>(const float v[8]) {
+  Vec8<float> r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    r.q[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                        __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+  return r;
 }
 
 // max that keeps a NaN (a group with a NaN gets a NaN scale, so that it reads
@@ -121,7 +168,7 @@ struct NormParams {
   float *scales;
   long long ldx, ldr, ldro, ldo;   // row strides in elements
   int T, H, group, n_groups;       // group: columns per scale, >= H for one scale a row
-  float eps;
+  float eps, inv_h;
 };
 
 // kTpr threads per row, kRows rows per block, kNe elements per thread.
@@ -157,13 +204,18 @@ __global__ void __launch_bounds__(kTpr *kRows) norm_kernel(const NormParams p) {
     }
 #pragma unroll
     for (int i = 0; i < kNv; ++i) {
+      float s[8], t[8];
+      unpack8(a[i], s);
+      if (r) {
+        unpack8(b[i], t);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] += t[j];
+      }
       const bool in = (tid + i * kTpr) * 8 < H;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        float s = in ? to_f32(a[i].v[j]) : 0.0f;
-        if (r && in) s += to_f32(b[i].v[j]);
-        v[8 * i + j] = s;
-        sq = fmaf(s, s, sq);
+        v[8 * i + j] = in ? s[j] : 0.0f;
+        sq = fmaf(v[8 * i + j], v[8 * i + j], sq);
       }
     }
   } else {
@@ -187,10 +239,7 @@ __global__ void __launch_bounds__(kTpr *kRows) norm_kernel(const NormParams p) {
 #pragma unroll
       for (int i = 0; i < kNe / 8; ++i) {
         const int c = (tid + i * kTpr) * 8;
-        Vec8<T> o;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o.v[j] = from_f32<T>(v[8 * i + j]);
-        if (c < H) store8(ro + c, o);
+        if (c < H) store8(ro + c, pack8<T>(v + 8 * i));
       }
     } else {
 #pragma unroll
@@ -201,7 +250,7 @@ __global__ void __launch_bounds__(kTpr *kRows) norm_kernel(const NormParams p) {
     }
   }
   sq = row_reduce<kTpr>(sq, SumOp(), s_red[0], tid);
-  const float inv = __fdiv_rn(1.0f, __fsqrt_rn(sq / (float)H + p.eps));
+  const float inv = rsqrtf(fmaf(sq, p.inv_h, p.eps));
 
   // y, and the 16- or 32-bit output
   if (kVec) {
@@ -212,13 +261,9 @@ __global__ void __launch_bounds__(kTpr *kRows) norm_kernel(const NormParams p) {
         const float4 w0 = __ldg(reinterpret_cast<const float4 *>(p.weight + c));
         const float4 w1 = __ldg(reinterpret_cast<const float4 *>(p.weight + c + 4));
         const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-        Vec8<T> o;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          v[8 * i + j] = v[8 * i + j] * inv * w[j];
-          o.v[j] = from_f32<T>(v[8 * i + j]);
-        }
-        if (out) store8(out + c, o);
+        for (int j = 0; j < 8; ++j) v[8 * i + j] = v[8 * i + j] * inv * w[j];
+        if (out) store8(out + c, pack8<T>(v + 8 * i));
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[8 * i + j] = 0.0f;
@@ -320,20 +365,48 @@ struct NormGradParams {
   float *partial;                // [gridDim.x][H] sums over each block's rows, or null
   long long ldh, lddo, ldds, lddx;
   int T, H;
-  float eps;
+  float eps, inv_h;
+  int stages;                    // rows in flight per block
 };
 
 // One block walks rows blockIdx.x, + gridDim.x, ...; a thread keeps its
 // columns' weights and weight-gradient sums in registers over all of them.
-// With kVec the next row's loads are issued before the current row is reduced,
-// so that memory is never idle through a reduction.
+// With kVec the rows come through a ring of shared-memory stages filled by bulk
+// copies, so that several rows of all three inputs are in flight while one is
+// reduced: on 8192 rows of 4096 bf16, plain loads with one row in registers
+// ahead took 98 us (waiting for loads), the ring takes GRAD_US us.  The barrier
+// of the row's reduction also frees its stage: every thread has its elements
+// in registers by then.
 template <typename T, int kTpr, int kNe, bool kVec, int kMinBlocks>
 __global__ void __launch_bounds__(kTpr, kMinBlocks) norm_grad_kernel(const NormGradParams p) {
-  constexpr int kWarps = kTpr / 32, kNv = kVec ? kNe / 8 : 1;
+  constexpr int kWarps = kTpr / 32;
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 s_red[2][kWarps];
+  __shared__ uint64_t full[kMaxStages];
+  const int tid = threadIdx.x, H = p.H;
+  const uint32_t row_bytes = (uint32_t)H * sizeof(T);
+  const bool direct = p.dsum != nullptr;
+  if (kVec) {
+    if (tid == 0) {
+      for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
+      fence_mbar_init();
+    }
+    __syncthreads();
+  }
   grid_dependency_wait();
   grid_dependency_launch();
-  const int tid = threadIdx.x, H = p.H;
+  const uint32_t stage_bytes = row_bytes * (direct ? 3 : 2);
+  auto fetch = [&](long long row, int st) {
+    if (row >= p.T) return;
+    uint8_t *dst = ring + st * stage_bytes;
+    mbar_arrive_expect_tx(&full[st], stage_bytes);
+    bulk_g2s(dst, static_cast<const T *>(p.h) + row * p.ldh, row_bytes, &full[st]);
+    bulk_g2s(dst + row_bytes, static_cast<const T *>(p.dout) + row * p.lddo, row_bytes, &full[st]);
+    if (direct)
+      bulk_g2s(dst + 2 * row_bytes, static_cast<const T *>(p.dsum) + row * p.ldds, row_bytes, &full[st]);
+  };
+  if (kVec && tid == 0)
+    for (int s = 0; s < p.stages; ++s) fetch(blockIdx.x + (long long)s * gridDim.x, s);
   auto col = [&](int i) { return kVec ? (tid + (i / 8) * kTpr) * 8 + i % 8 : tid + i * kTpr; };
   float dg[kNe], w[kNe];
 #pragma unroll
@@ -341,38 +414,26 @@ __global__ void __launch_bounds__(kTpr, kMinBlocks) norm_grad_kernel(const NormG
     dg[i] = 0.0f;
     w[i] = col(i) < H ? __ldg(p.weight + col(i)) : 0.0f;
   }
-  Vec8<T> hn[kNv], dn[kNv], sn[kNv];   // the next row
-  const bool direct = p.dsum != nullptr;
-  auto fetch = [&](long long row) {
-    if (!kVec || row >= p.T) return;
-    const T *h = static_cast<const T *>(p.h) + row * p.ldh;
-    const T *dy = static_cast<const T *>(p.dout) + row * p.lddo;
-    const T *ds = static_cast<const T *>(p.dsum) + row * p.ldds;
-#pragma unroll
-    for (int i = 0; i < kNv; ++i) {
-      const int c = col(8 * i);
-      if (c < H) {
-        hn[i] = load8(h + c);
-        dn[i] = load8(dy + c);
-        if (direct) sn[i] = load8(ds + c);
-      }
-    }
-  };
-  fetch(blockIdx.x);
-  int flip = 0;
+  int flip = 0, st = 0;
+  uint32_t phase = 0;
   for (long long row = blockIdx.x; row < p.T; row += gridDim.x, flip ^= 1) {
     float a[kNe], d[kNe];
-    Vec8<T> sc[kNv];
+    Vec8<T> sc[kVec ? kNe / 8 : 1];
     if (kVec) {
+      if (!mbar_wait(&full[st], phase, nullptr)) break;
+      const T *sh = reinterpret_cast<const T *>(ring + st * stage_bytes);
 #pragma unroll
-      for (int i = 0; i < kNe; ++i) {
-        const bool in = col(i - i % 8) < H;
-        a[i] = in ? to_f32(hn[i / 8].v[i % 8]) : 0.0f;
-        d[i] = in ? to_f32(dn[i / 8].v[i % 8]) : 0.0f;
+      for (int i = 0; i < kNe; i += 8) {
+        const bool in = col(i) < H;
+        if (in) {
+          unpack8(load8(sh + col(i)), a + i);
+          unpack8(load8(sh + H + col(i)), d + i);
+          if (direct) sc[i / 8] = load8(sh + 2 * H + col(i));
+        } else {
+#pragma unroll
+          for (int j = i; j < i + 8; ++j) a[j] = d[j] = 0.0f;
+        }
       }
-#pragma unroll
-      for (int i = 0; i < kNv; ++i) sc[i] = sn[i];
-      fetch(row + gridDim.x);
     } else {
       const T *h = static_cast<const T *>(p.h) + row * p.ldh;
       const T *dy = static_cast<const T *>(p.dout) + row * p.lddo;
@@ -392,10 +453,17 @@ __global__ void __launch_bounds__(kTpr, kMinBlocks) norm_grad_kernel(const NormG
       sq += __shfl_xor_sync(0xffffffffu, sq, o);
       dot += __shfl_xor_sync(0xffffffffu, dot, o);
     }
+    // (two slots in turn: a warp is at most one row ahead of the others)
+    if (kWarps > 1 && (tid & 31) == 0) s_red[flip][tid >> 5] = make_float2(sq, dot);
+    if (kWarps > 1 || kVec) __syncthreads();
+    if (kVec) {
+      if (tid == 0) fetch(row + (long long)p.stages * gridDim.x, st);
+      if (++st == p.stages) {
+        st = 0;
+        phase ^= 1u;
+      }
+    }
     if (kWarps > 1) {
-      // (two slots in turn: a warp is at most one row ahead of the others)
-      if ((tid & 31) == 0) s_red[flip][tid >> 5] = make_float2(sq, dot);
-      __syncthreads();
       const float2 v = s_red[flip][tid & (kWarps - 1)];
       sq = v.x;
       dot = v.y;
@@ -405,26 +473,25 @@ __global__ void __launch_bounds__(kTpr, kMinBlocks) norm_grad_kernel(const NormG
         dot += __shfl_xor_sync(0xffffffffu, dot, o);
       }
     }
-    const float inv = __fdiv_rn(1.0f, __fsqrt_rn(sq / (float)H + p.eps));
-    const float back = dot * inv * inv / (float)H;   // i^2 mean(gy h)
+    const float inv = rsqrtf(fmaf(sq, p.inv_h, p.eps));
+    const float back = dot * p.inv_h * inv * inv;   // i^2 mean(gy h)
     T *dx = static_cast<T *>(p.dx) + row * p.lddx;
     const T *ds = static_cast<const T *>(p.dsum) + row * p.ldds;
-    Vec8<T> e[kNv];
 #pragma unroll
-    for (int i = 0; i < kNe; ++i) {
-      dg[i] = fmaf(d[i], a[i] * inv, dg[i]);
-      float o = inv * (d[i] * w[i] - a[i] * back);
-      if (kVec) {
-        if (direct) o += to_f32(sc[i / 8].v[i % 8]);
-        e[i / 8].v[i % 8] = from_f32<T>(o);
-      } else if (col(i) < H) {
-        dx[col(i)] = from_f32<T>(direct ? o + to_f32(ds[col(i)]) : o);
+    for (int i = 0; i < kNe; i += 8) {
+      float o[8], s[8];
+      if (kVec && direct) unpack8(sc[i / 8], s);
+#pragma unroll
+      for (int j = i; j < i + 8; ++j) {
+        dg[j] = fmaf(d[j], a[j] * inv, dg[j]);
+        o[j - i] = inv * (d[j] * w[j] - a[j] * back);
+        if (kVec) {
+          if (direct) o[j - i] += s[j - i];
+        } else if (col(j) < H) {
+          dx[col(j)] = from_f32<T>(direct ? o[j - i] + to_f32(ds[col(j)]) : o[j - i]);
+        }
       }
-    }
-    if (kVec) {
-#pragma unroll
-      for (int i = 0; i < kNv; ++i)
-        if (col(8 * i) < H) store8(dx + col(8 * i), e[i]);
+      if (kVec && col(i) < H) store8(dx + col(i), pack8<T>(o));
     }
   }
   if (p.partial) {
@@ -463,20 +530,31 @@ __global__ void __launch_bounds__(1024) norm_grad_sum_kernel(const float *partia
 // sums are as long as a row and are read again).
 inline int grad_blocks(int T) { return T >= 1184 ? 296 : T < 148 ? T : 148; }
 
+template <typename T, int kTpr, int kNe, bool kVec, int kMinBlocks>
+cudaError_t launch_norm_grad_as(NormGradParams p, cudaStream_t stream) {
+  auto kern = norm_grad_kernel<T, kTpr, kNe, kVec, kMinBlocks>;
+  int smem = 0;
+  if (kVec) {
+    // two blocks share a multiprocessor's 227 KB, or one takes it (a row of
+    // 16384 fp32 elements and its two gradients are 192 KB)
+    const int stage = p.H * (int)sizeof(T) * (p.dsum ? 3 : 2);
+    p.stages = std::min(kMaxStages, std::max(1, (kMinBlocks > 1 ? 110 : 220) * 1024 / stage));
+    smem = p.stages * stage;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(kern, dim3(grad_blocks(p.T)), dim3(kTpr), smem, stream, p);
+}
+
 template <typename T, bool kVec>
 cudaError_t launch_norm_grad(const NormGradParams &p, cudaStream_t stream) {
-  const dim3 grid(grad_blocks(p.T));
-  if (p.H <= 256) return launch_pdl(norm_grad_kernel<T, 32, 8, kVec, 2>, grid, dim3(32), 0, stream, p);
-  if (p.H <= 512) return launch_pdl(norm_grad_kernel<T, 64, 8, kVec, 2>, grid, dim3(64), 0, stream, p);
-  if (p.H <= 1024) return launch_pdl(norm_grad_kernel<T, 128, 8, kVec, 2>, grid, dim3(128), 0, stream, p);
-  if (p.H <= 2048) return launch_pdl(norm_grad_kernel<T, 256, 8, kVec, 2>, grid, dim3(256), 0, stream, p);
-  if (p.H <= 4096) {
-    if (sizeof(T) == 2)
-      return launch_pdl(norm_grad_kernel<T, 256, 16, kVec, 2>, grid, dim3(256), 0, stream, p);
-    return launch_pdl(norm_grad_kernel<T, 512, 8, kVec, 1>, grid, dim3(512), 0, stream, p);
-  }
-  if (p.H <= 8192) return launch_pdl(norm_grad_kernel<T, 512, 16, kVec, 1>, grid, dim3(512), 0, stream, p);
-  return launch_pdl(norm_grad_kernel<T, 1024, 16, kVec, 1>, grid, dim3(1024), 0, stream, p);
+  if (p.H <= 256) return launch_norm_grad_as<T, 32, 8, kVec, 2>(p, stream);
+  if (p.H <= 512) return launch_norm_grad_as<T, 64, 8, kVec, 2>(p, stream);
+  if (p.H <= 1024) return launch_norm_grad_as<T, 64, 16, kVec, 2>(p, stream);
+  if (p.H <= 2048) return launch_norm_grad_as<T, 128, 16, kVec, 2>(p, stream);
+  if (p.H <= 4096) return launch_norm_grad_as<T, 256, 16, kVec, 2>(p, stream);
+  if (p.H <= 8192) return launch_norm_grad_as<T, 512, 16, kVec, 1>(p, stream);
+  return launch_norm_grad_as<T, 1024, 16, kVec, 1>(p, stream);
 }
 
 // ---------------------------------------------------------------- unpack
@@ -582,6 +660,7 @@ strata_status strata_rmsnorm(int dtype, const void *x, long long x_stride, const
   p.group = out_q8 ? group : hidden;
   p.n_groups = (hidden + p.group - 1) / p.group;
   p.eps = eps;
+  p.inv_h = (float)(1.0 / hidden);
   const bool vec = hidden % 8 == 0 && rows_vec(x, x_stride, b) &&
                    rows_vec(residual, residual_stride, b) &&
                    rows_vec(residual_out, residual_out_stride, b) && rows_vec(out, out_stride, b) &&
@@ -641,6 +720,7 @@ strata_status strata_rmsnorm_backward(int dtype, const void *h, long long h_stri
   p.T = n_tokens;
   p.H = hidden;
   p.eps = eps;
+  p.inv_h = (float)(1.0 / hidden);
   const bool vec = hidden % 8 == 0 && rows_vec(h, h_stride, b) && rows_vec(dout, dout_stride, b) &&
                    rows_vec(dsum, dsum_stride, b) && rows_vec(dx, dx_stride, b);
   cudaError_t e;

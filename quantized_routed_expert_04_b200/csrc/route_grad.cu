@@ -30,7 +30,7 @@ namespace strata {
 
 namespace {
 
-constexpr int kPrepWarps = 8;
+constexpr int kPrepWarps = 16;
 
 __device__ __forceinline__ uint32_t bf162_bits(__nv_bfloat162 v) {
   return *reinterpret_cast<uint32_t *>(&v);
@@ -50,6 +50,48 @@ __device__ __forceinline__ uint4 take_bf16(float v[8]) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// The gradient of token t's selected logits through its routing weights: lane
+// j < k gets selection j's expert (-1: none) and gradient.
+__device__ __forceinline__ void weight_grad(const RouteGradParams &p, int t, int lane, int &id,
+                                            float &g) {
+  const bool sel = lane < p.k;
+  id = sel ? p.idx[(size_t)t * p.k + lane] : -1;
+  const float dw = sel ? p.dw[(size_t)t * p.k + lane] : 0.0f;
+  const bool bad = sel && (id < 0 || id >= p.E);
+  // (a token with a bad id: the forward writes it a zero row, dw has no meaning)
+  const bool any_bad = __any_sync(0xffffffffu, bad);
+  if (bad) set_status(p.status, STATUS_BAD_ROUTING);
+  const bool use = sel && !any_bad;
+  const float l = use ? p.logits[(size_t)t * p.E + id] : 0.0f;
+  float w, slope;   // w_j / scale, and its factor in the gradient
+  if (p.mode.sigmoid) {
+    const float ex = expf(-l);
+    const float s = use ? __fdiv_rn(1.0f, 1.0f + ex) : 0.0f;
+    const float z = warp_sum(s);
+    // (a true division: one selected expert has w = 1 and no gradient)
+    w = z == 0.0f ? 0.0f : __fdiv_rn(s, z);
+    slope = s == 0.0f ? 0.0f : p.mode.scale * w * (ex * s);
+  } else {
+    float m = use ? l : __int_as_float(0xff800000);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const bool none = m == __int_as_float(0xff800000);
+    const float ex = !use || (none && l == m) ? 0.0f : expf(l - m);
+    const float z = warp_sum(ex);
+    w = z == 0.0f ? 0.0f : __fdiv_rn(ex, z);
+    slope = w;
+  }
+  const float dot = warp_sum(use ? w * dw : 0.0f);
+  g = use ? slope * (dw - dot) : 0.0f;
+  id = use ? id : -1;
+}
+
 // Blocks 0 .. tok_blocks - 1: rows of dl, one warp per token at a time, each
 // lane 8 consecutive experts, as three bf16 pieces, and the block's share of
 // db.  The blocks behind them: W as two bf16 pieces.
@@ -57,7 +99,7 @@ __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const 
   __shared__ float s_db[kPrepWarps][kMaxExperts];
   grid_dependency_wait();
   grid_dependency_launch();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = p.E, k = p.k;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = p.E;
   if ((int)blockIdx.x >= p.tok_blocks) {
     const size_t n8 = (size_t)E * p.H / 8;
     const size_t step = (size_t)(gridDim.x - p.tok_blocks) * blockDim.x;
@@ -70,60 +112,34 @@ __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const 
     }
     return;
   }
+  const bool vec = E % 8 == 0 && (reinterpret_cast<uintptr_t>(p.dlogits) & 15) == 0;
   float db[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) db[i] = 0.0f;
   for (int t = blockIdx.x * kPrepWarps + warp; t < p.T; t += p.tok_blocks * kPrepWarps) {
-    // lane j < k: selection j
-    int id = -1;
-    float g = 0.0f;
-    if (p.dw) {
-      const bool sel = lane < k;
-      id = sel ? p.idx[(size_t)t * k + lane] : -1;
-      const bool bad = sel && (id < 0 || id >= E);
-      if (__any_sync(0xffffffffu, bad)) {
-        // the forward writes a zero row for such a token: dw has no meaning
-        if (bad) set_status(p.status, STATUS_BAD_ROUTING);
-        id = -1;
-      } else {
-        const float l = sel ? p.logits[(size_t)t * E + id] : 0.0f;
-        const float dw = sel ? p.dw[(size_t)t * k + lane] : 0.0f;
-        float w, slope;   // w_j / scale, and its factor in the gradient
-        if (p.mode.sigmoid) {
-          const float ex = expf(-l);
-          const float s = sel ? __fdiv_rn(1.0f, 1.0f + ex) : 0.0f;
-          float z = s;
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-          // (a true division: one selected expert has w = 1 and no gradient)
-          w = z == 0.0f ? 0.0f : __fdiv_rn(s, z);
-          slope = s == 0.0f ? 0.0f : p.mode.scale * w * (ex * s);
-        } else {
-          float m = sel ? l : __int_as_float(0xff800000);
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          const bool none = m == __int_as_float(0xff800000);
-          const float ex = !sel || (none && l == m) ? 0.0f : expf(l - m);
-          float z = ex;
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-          w = z == 0.0f ? 0.0f : __fdiv_rn(ex, z);
-          slope = w;
-        }
-        float dot = sel ? w * dw : 0.0f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        g = sel ? slope * (dw - dot) : 0.0f;
-      }
-    }
     float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = 8 * lane + i;
-      v[i] = p.dlogits && e < E ? p.dlogits[(size_t)t * E + e] : 0.0f;
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    if (p.dlogits) {
+      const float *row = p.dlogits + (size_t)t * E + 8 * lane;
+      if (vec) {
+        if (8 * lane < E) {
+          const float4 a = reinterpret_cast<const float4 *>(row)[0];
+          const float4 b = reinterpret_cast<const float4 *>(row)[1];
+          v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+          v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (8 * lane + i < E) v[i] = row[i];
+      }
     }
     if (p.dw) {
-      for (int j = 0; j < k; ++j) {
+      int id;
+      float g;
+      weight_grad(p, t, lane, id, g);
+      for (int j = 0; j < p.k; ++j) {
         const int at = __shfl_sync(0xffffffffu, id, j) - 8 * lane;
         const float gj = __shfl_sync(0xffffffffu, g, j);
 #pragma unroll
@@ -133,11 +149,11 @@ __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const 
 #pragma unroll
     for (int i = 0; i < 8; ++i) db[i] += v[i];
     if (p.dlp && 8 * lane < E) {
-      const size_t row = (size_t)p.T * p.Epad / 8;
+      const size_t plane = (size_t)p.T * p.Epad / 8;
       uint4 *out = reinterpret_cast<uint4 *>(p.dlp) + (size_t)t * (p.Epad / 8) + lane;
       out[0] = take_bf16(v);
-      out[row] = take_bf16(v);
-      out[2 * row] = take_bf16(v);
+      out[plane] = take_bf16(v);
+      out[2 * plane] = take_bf16(v);
     }
   }
   if (p.db_part) {
@@ -154,11 +170,19 @@ __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const 
 }
 
 // ---------------------------------------------------------------- tensor cores
-// Both GEMMs read at least one operand along its rows, the K index running
-// down them ("MN-major"): a box of 64 elements x R rows lands as R rows of 128
-// bytes, 128-byte swizzled in groups of 8 rows.  The descriptor's leading
-// offset is the distance between such boxes (64 elements further along M or
-// N), its stride offset that between groups of 8 rows (8 further along K).
+// Both products run on pairs of blocks (clusters of two, tcgen05 cta_group::2):
+// one MMA covers M = 256 rows of h, 128 in each block's tensor memory, and up
+// to N = 256 columns, whose operand each block loads half of.  So the streamed
+// operand crosses from L2 half as often as with one block per tile, which is
+// what bounded that form.  Every block loads its own share into its own shared
+// memory and counts the bytes on the first block's barrier; the first block's
+// MMA thread issues for both, and its commits arrive at both.
+//
+// Both read at least one operand along its rows, the K index running down them
+// ("MN-major"): a box of 64 elements x R rows lands as R rows of 128 bytes,
+// 128-byte swizzled in groups of 8 rows.  The descriptor's leading offset is
+// the distance between such boxes (64 elements further along M or N), its
+// stride offset that between groups of 8 rows (8 further along K).
 __device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t smem_addr, uint32_t box_bytes) {
   uint64_t d = 0;
   d |= (uint64_t)((smem_addr >> 4) & 0x3FFF);
@@ -173,13 +197,71 @@ __device__ __forceinline__ uint32_t umma_idesc_bf16(int M, int N, bool a_mn, boo
   return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, int c0, int c1, int c2,
-                                            uint64_t *bar) {
+__device__ __forceinline__ void umma2_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-      "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// Arrive on the barrier at this place in both blocks once all earlier MMAs of
+// this thread have completed.
+__device__ __forceinline__ void umma2_commit(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_arrive(uint32_t bar_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_addr) : "memory");
+}
+// Loads into this block's shared memory, counted on a barrier of either block
+// of the pair (a shared::cluster address).
+__device__ __forceinline__ void tma2_load_2d(void *dst, const void *tmap, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma2_load_3d(void *dst, const void *tmap, int c0, int c1, int c2,
+                                             uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+// 16 columns of this warp's 32 tensor-memory lanes (one lane a thread).
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, float v[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 struct Ring {
@@ -192,142 +274,223 @@ struct Ring {
   }
 };
 
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 8;
 constexpr int kSmemLimit = 232448;
-constexpr uint32_t kTmem = 512;
+constexpr uint32_t kTmem = 512;       // two accumulators of 256 columns
+constexpr int kTileH = 256;           // rows of h per pair of blocks
+constexpr int kEpiWarps = 8;
+constexpr int kTcThreads = 32 * (2 + kEpiWarps);   // producer, MMA, epilogue
 
-// dW[e][h] = sum_t dl[t][e] x[t][h]: M = 128 rows of h (two accumulators: 256
-// h a block), N = the experts, K = tokens.  All experts sit in one tile, so x
-// is read from memory once; the tokens are split over blocks until the
-// multiprocessors are full.  Stages of 32 tokens: x as 4 boxes, each piece of
-// dl as experts / 64 boxes.
-constexpr int kDwTok = 32;
-constexpr int kDwBox = kDwTok * 128;
-constexpr int kDwH = 256;
-constexpr int kDwThreads = 192;   // producer, MMA, 4 epilogue warps
-
-struct DwParams {
-  int T, H, E, splits, stages;
-  float *out;         // [splits][E][H]
-  int *status;
+// Barriers of a block (those that count arrivals of both blocks live in the
+// first one) and the pair's tensor memory.
+struct PairShared {
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], w_full, w_empty;
+  uint32_t tmem;
 };
 
-__global__ void __launch_bounds__(kDwThreads, 1)
+__device__ __forceinline__ void pair_begin(PairShared &s, int stages, int warp) {
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.acc_full[i], 1);
+      mbar_init(&s.acc_empty[i], 2 * kEpiWarps);
+    }
+    mbar_init(&s.w_full, 1);
+    mbar_init(&s.w_empty, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s.tmem)),
+                 "r"(kTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // both blocks' barriers are set up before either signals
+  tc_fence_after();
+}
+__device__ __forceinline__ void pair_end(PairShared &s, int warp) {
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // neither block leaves while the other may still reach it
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(s.tmem), "r"(kTmem)
+                 : "memory");
+  }
+}
+// One lane waits, the warp learns the outcome.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int lane, int *status) {
+  const int ok = lane == 0 ? (mbar_wait(bar, parity, status) ? 1 : 0) : 0;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// dW[e][h] = sum_t dl[t][e] x[t][h]: M = 256 rows of h, N = the experts (all of
+// them, so x is read from memory once), K = tokens in stages of 32.  The stages
+// of all h tiles in one row are cut into equal runs, one per pair of blocks; a
+// run's part of a tile goes to slot run + tile of the workspace (or straight to
+// dW if it is the whole tile), and the last kernel adds the slots in order.
+//
+// The tensor core cuts its running sum at every MMA (2^-23 relative, always
+// towards zero): over one chain of 910 tokens, 168 MMAs, dW came out 2.7e-6 too
+// small.  So a chain is kDwChain stages (48 MMAs); the epilogue warps add the
+// chains in fp32 registers, rounding to nearest, while the other accumulator
+// takes the next chain.
+constexpr int kDwTok = 32;
+constexpr int kDwBox = kDwTok * 128;   // 64 columns
+constexpr int kDwChain = 8;
+
+struct DwParams {
+  int T, H, E, pairs, stages;
+  float *out;          // dW
+  float *part;         // [pairs + tiles - 1][E][256]
+  int *status;
+};
+__host__ __device__ inline long long run_begin(long long units, int pairs, int i) {
+  return units * i / pairs;
+}
+
+// kBoxes: boxes of 64 experts per block (N = 128 kBoxes)
+template <int kBoxes>
+__global__ void __launch_bounds__(kTcThreads, 1)
     route_grad_dw_kernel(const DwParams p, const __grid_constant__ CUtensorMap map_x,
                          const __grid_constant__ CUtensorMap map_dl) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full;
-  __shared__ uint32_t s_tmem;
+  __shared__ PairShared s;
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-    }
-    mbar_init(&acc_full, 1);
-    fence_mbar_init();
     prefetch_tmap(&map_x);
     prefetch_tmap(&map_dl);
   }
-  if (warp == 1) {
-    tmem_alloc(&s_tmem, kTmem);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  pair_begin(s, p.stages, warp);
+  const uint32_t tmem = s.tmem, rank = cluster_rank();
   grid_dependency_wait();
   grid_dependency_launch();
 
-  const int h0 = blockIdx.x * kDwH, split = blockIdx.y;
-  const int n_acc = p.H - h0 >= kDwH ? 2 : 1;
-  const int nb = (p.E + 63) / 64;                     // boxes of 64 experts
+  constexpr int kStage = (2 + 3 * kBoxes) * kDwBox;   // per block
   const int n_kb = (p.T + kDwTok - 1) / kDwTok;
-  const int kb0 = (int)((long long)split * n_kb / p.splits);
-  const int kb1 = (int)((long long)(split + 1) * n_kb / p.splits);
-  const int stage_bytes = (kDwH / 64 + 3 * nb) * kDwBox;
+  const int tiles = (p.H + kTileH - 1) / kTileH;
+  const int pair = blockIdx.x >> 1;
+  const long long units = (long long)tiles * n_kb;
+  const long long u0 = run_begin(units, p.pairs, pair), u1 = run_begin(units, p.pairs, pair + 1);
   if (warp == 0) {
     if (lane == 0) {
       Ring r;
-      int issued = 0;
+      long long issued = 0;
       bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(&empty[r.st], r.ph ^ 1u, p.status)) { ok = false; break; }
-        uint8_t *a = smem + r.st * stage_bytes, *b = a + kDwH / 64 * kDwBox;
-        mbar_arrive_expect_tx(&full[r.st], (uint32_t)((2 * n_acc + 3 * nb) * kDwBox));
-        for (int i = 0; i < 2 * n_acc; ++i)
-          tma_load_2d(a + i * kDwBox, &map_x, h0 + 64 * i, kb * kDwTok, &full[r.st]);
+      for (long long u = u0; u < u1; ++u) {
+        if (!mbar_wait(&s.empty[r.st], r.ph ^ 1u, p.status)) { ok = false; break; }
+        const int tile = (int)(u / n_kb), t = (int)(u - (long long)tile * n_kb) * kDwTok;
+        uint8_t *a = smem + r.st * kStage, *b = a + 2 * kDwBox;
+        const uint32_t bar = cluster_addr(&s.full[r.st], 0);
+        if (rank == 0) mbar_arrive_expect_tx(&s.full[r.st], 2 * kStage);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          tma2_load_2d(a + i * kDwBox, &map_x, tile * kTileH + 128 * (int)rank + 64 * i, t, bar);
+#pragma unroll
         for (int c = 0; c < 3; ++c)
-          for (int i = 0; i < nb; ++i)
-            tma_load_3d(b + (c * nb + i) * kDwBox, &map_dl, 64 * i, kb * kDwTok, c, &full[r.st]);
+#pragma unroll
+          for (int i = 0; i < kBoxes; ++i)
+            tma2_load_3d(b + (c * kBoxes + i) * kDwBox, &map_dl, 64 * (kBoxes * (int)rank + i), t, c, bar);
         ++issued;
         r.next(p.stages);
       }
-      if (!ok)   // let issued copies land before the block exits
-        for (int m = issued > p.stages ? issued - p.stages : 0; m < issued; ++m)
-          (void)mbar_wait(&full[m % p.stages], (m / p.stages) & 1u, p.status);
+      if (!ok && rank == 0)   // let issued copies land
+        for (long long m = issued > p.stages ? issued - p.stages : 0; m < issued; ++m)
+          (void)mbar_wait(&s.full[m % p.stages], (uint32_t)(m / p.stages) & 1u, p.status);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       Ring r;
-      const uint32_t idesc = umma_idesc_bf16(128, 64 * nb, true, true);
+      const uint32_t idesc = umma_idesc_bf16(256, 128 * kBoxes, true, true);
+      int n = 0;   // chains
       bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(&full[r.st], r.ph, p.status)) { ok = false; break; }
+      for (long long u = u0; u < u1 && ok; ++n) {
+        const int tile = (int)(u / n_kb);
+        const long long end = min(min(u1, (long long)(tile + 1) * n_kb), u + kDwChain);
+        const int buf = n & 1;
+        if (!mbar_wait(&s.acc_empty[buf], ((n >> 1) & 1u) ^ 1u, p.status)) break;
         tc_fence_after();
-        const uint32_t a = smem_u32(smem + r.st * stage_bytes), b = a + kDwH / 64 * kDwBox;
+        const uint32_t d = tmem + buf * 256;
+        uint32_t more = 0u;
+        for (; u < end; ++u) {
+          if (!mbar_wait(&s.full[r.st], r.ph, p.status)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a = smem_u32(smem + r.st * kStage);
+          const uint64_t ad = umma_desc_mn_sw128(a, kDwBox);
+          const uint64_t bd = umma_desc_mn_sw128(a + 2 * kDwBox, kDwBox);
 #pragma unroll
-        for (int ks = 0; ks < kDwTok / 16; ++ks)
-          for (int c = 0; c < 3; ++c) {
-            const uint64_t bd = umma_desc_mn_sw128(b + c * nb * kDwBox + ks * 2048, kDwBox);
-            for (int m = 0; m < n_acc; ++m)
-              umma_f16(tmem + m * 256, umma_desc_mn_sw128(a + m * 2 * kDwBox + ks * 2048, kDwBox), bd,
-                       idesc, kb > kb0 || ks > 0 || c > 0 ? 1u : 0u);
-          }
-        umma_commit(&empty[r.st]);
-        r.next(p.stages);
+          for (int c = 0; c < 3; ++c)
+#pragma unroll
+            for (int ks = 0; ks < kDwTok / 16; ++ks) {
+              umma2_f16(d, ad + ks * (2048 >> 4), bd + c * (kBoxes * kDwBox >> 4) + ks * (2048 >> 4), idesc, more);
+              more = 1u;
+            }
+          umma2_commit(&s.empty[r.st]);
+          r.next(p.stages);
+        }
+        if (ok) umma2_commit(&s.acc_full[buf]);
       }
-      if (ok) umma_commit(&acc_full);
     }
   } else {
-    // lane: one h of its quarter; column: one expert -> 128 consecutive bytes
-    const int qd = warp & 3;
-    const int okw = lane == 0 ? (mbar_wait(&acc_full, 0u, p.status) ? 1 : 0) : 0;
-    if (__shfl_sync(0xffffffffu, okw, 0)) {
-      tc_fence_after();
-      for (int m = 0; m < n_acc; ++m) {
-        float *out = p.out + (size_t)split * p.E * p.H + h0 + 128 * m + 32 * qd + lane;
-        for (int c0 = 0; c0 < p.E; c0 += 32) {
-          float v[32];
-          tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * qd) << 16) + m * 256 + c0, v);
+    // lane: one h; column: one expert.  Each warp holds a quarter of the lanes
+    // and half of the columns.
+    constexpr int kCols = 64 * kBoxes;
+    const int qd = warp & 3, half = (warp - 2) >> 2;
+    const int hh = 128 * (int)rank + 32 * qd + lane;
+    const uint32_t empty_bar[2] = {cluster_addr(&s.acc_empty[0], 0), cluster_addr(&s.acc_empty[1], 0)};
+    int n = 0;
+    bool ok = true;
+    for (long long u = u0; u < u1 && ok;) {
+      const int tile = (int)(u / n_kb);
+      const long long tile0 = (long long)tile * n_kb, end = min(u1, tile0 + n_kb);
+      const bool whole = u == tile0 && end == tile0 + n_kb;
+      float acc[kCols];
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c0 + i < p.E) out[(size_t)(c0 + i) * p.H] = v[i];
+      for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
+      for (; u < end; u += kDwChain, ++n) {
+        const int buf = n & 1;
+        if (!warp_wait(&s.acc_full[buf], (n >> 1) & 1u, lane, p.status)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < kCols; c += 16) {
+          float v[16];
+          tmem_ld_32x32b_x16(tmem + ((uint32_t)(32 * qd) << 16) + buf * 256 + half * kCols + c, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[c + i] += v[i];
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) cluster_arrive(empty_bar[buf]);
       }
+      u = end;
+      const int h = tile * kTileH + hh;
+      if (!ok || h >= p.H) continue;
+      float *out = whole ? p.out + h : p.part + ((size_t)(pair + tile) * p.E) * kTileH + hh;
+      const size_t ld = whole ? p.H : kTileH;
+#pragma unroll
+      for (int i = 0; i < kCols; ++i)
+        if (half * kCols + i < p.E) out[(size_t)(half * kCols + i) * ld] = acc[i];
     }
-    tc_fence_before();
   }
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, kTmem);
-  }
+  pair_end(s, warp);
 }
 
-// dx[t][h] = sum_e dl[t][e] W[e][h]: M = 128 rows of h, N = 256 tokens, K = the
-// experts.  The block's W (both pieces, every expert) stays in shared memory
-// while blocks of 256 tokens of dl stream past it in stages of 64 experts of
-// one piece.  Work items (h tile, token tile), h-major, in one contiguous run
-// per block: W is loaded again only where a run crosses into the next h tile.
-constexpr int kDxTok = 256, kDxH = 128;
-constexpr int kDxStage = kDxTok * 128;
+// dx[t][h] = sum_e dl[t][e] W[e][h]: M = 256 rows of h, N = 256 tokens, K = the
+// experts.  A block's 128 rows of W (both pieces, every expert) stay in shared
+// memory while blocks of 256 tokens of dl stream past it in stages of 64
+// experts of one piece.  Work items (h tile, token tile), h-major, in one
+// contiguous run per pair: W is loaded again only where a run crosses into the
+// next h tile.
+constexpr int kDxTok = 256;
+constexpr int kDxStage = kDxTok / 2 * 128;   // per block
 constexpr int kDxWBox = 64 * 128;
-constexpr int kDxEpiWarps = 8;
-constexpr int kDxThreads = 32 * (2 + kDxEpiWarps);
 
 struct DxParams {
   int T, H, E, stages;
@@ -335,47 +498,31 @@ struct DxParams {
   int *status;
 };
 
-__global__ void __launch_bounds__(kDxThreads, 1)
+__global__ void __launch_bounds__(kTcThreads, 1)
     route_grad_dx_kernel(const DxParams p, const __grid_constant__ CUtensorMap map_dl,
                          const __grid_constant__ CUtensorMap map_w) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], w_full, w_empty;
-  __shared__ uint32_t s_tmem;
+  __shared__ PairShared s;
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-    }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&acc_full[s], 1);
-      mbar_init(&acc_empty[s], kDxEpiWarps);
-    }
-    mbar_init(&w_full, 1);
-    mbar_init(&w_empty, 1);
-    fence_mbar_init();
     prefetch_tmap(&map_dl);
     prefetch_tmap(&map_w);
   }
-  if (warp == 1) {
-    tmem_alloc(&s_tmem, kTmem);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  pair_begin(s, p.stages, warp);
+  const uint32_t tmem = s.tmem, rank = cluster_rank();
   grid_dependency_wait();
   grid_dependency_launch();
 
   const int n_kb = (p.E + 63) / 64;
   const int t_tiles = (p.T + kDxTok - 1) / kDxTok;
-  const long long items = (long long)t_tiles * (p.H / kDxH);
-  const long long i0 = items * blockIdx.x / gridDim.x, i1 = items * (blockIdx.x + 1) / gridDim.x;
+  const long long items = (long long)t_tiles * ((p.H + kTileH - 1) / kTileH);
+  const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+  const long long i0 = run_begin(items, pairs, pair), i1 = run_begin(items, pairs, pair + 1);
+  const uint32_t w_bytes = 2 * n_kb * 2 * kDxWBox;
   uint8_t *w_smem = smem;                              // [piece][k block][h half]
-  uint8_t *ring = smem + 2 * n_kb * 2 * kDxWBox;
+  uint8_t *ring = smem + w_bytes;
   if (warp == 0) {
     if (lane == 0) {
       Ring r;
@@ -385,34 +532,36 @@ __global__ void __launch_bounds__(kDxThreads, 1)
       for (long long i = i0; i < i1 && ok; ++i) {
         const int h = (int)(i / t_tiles), t = (int)(i - (long long)h * t_tiles);
         if (h != cur) {
-          if (cur >= 0 && !mbar_wait(&w_empty, (w_uses - 1) & 1u, p.status)) { ok = false; break; }
+          if (cur >= 0 && !mbar_wait(&s.w_empty, (w_uses - 1) & 1u, p.status)) { ok = false; break; }
           cur = h;
           ++w_uses;
-          mbar_arrive_expect_tx(&w_full, (uint32_t)(2 * n_kb * 2 * kDxWBox));
+          const uint32_t bar = cluster_addr(&s.w_full, 0);
+          if (rank == 0) mbar_arrive_expect_tx(&s.w_full, 2 * w_bytes);
           for (int c = 0; c < 2; ++c)
             for (int kb = 0; kb < n_kb; ++kb)
               for (int m = 0; m < 2; ++m)
-                tma_load_3d(w_smem + ((c * n_kb + kb) * 2 + m) * kDxWBox, &map_w, h * kDxH + 64 * m,
-                            64 * kb, c, &w_full);
+                tma2_load_3d(w_smem + ((c * n_kb + kb) * 2 + m) * kDxWBox, &map_w,
+                             h * kTileH + 128 * (int)rank + 64 * m, 64 * kb, c, bar);
         }
         for (int q = 0; q < 2 * n_kb; ++q) {
-          if (!mbar_wait(&empty[r.st], r.ph ^ 1u, p.status)) { ok = false; break; }
-          mbar_arrive_expect_tx(&full[r.st], kDxStage);
-          tma_load_3d(ring + r.st * kDxStage, &map_dl, 64 * (q >> 1), t * kDxTok, q & 1, &full[r.st]);
+          if (!mbar_wait(&s.empty[r.st], r.ph ^ 1u, p.status)) { ok = false; break; }
+          if (rank == 0) mbar_arrive_expect_tx(&s.full[r.st], 2 * kDxStage);
+          tma2_load_3d(ring + r.st * kDxStage, &map_dl, 64 * (q >> 1), t * kDxTok + kDxTok / 2 * (int)rank,
+                       q & 1, cluster_addr(&s.full[r.st], 0));
           ++issued;
           r.next(p.stages);
         }
       }
-      if (!ok) {
+      if (!ok && rank == 0) {
         for (long long m = issued > p.stages ? issued - p.stages : 0; m < issued; ++m)
-          (void)mbar_wait(&full[m % p.stages], (uint32_t)(m / p.stages) & 1u, p.status);
-        if (w_uses) (void)mbar_wait(&w_full, (w_uses - 1) & 1u, p.status);
+          (void)mbar_wait(&s.full[m % p.stages], (uint32_t)(m / p.stages) & 1u, p.status);
+        if (w_uses) (void)mbar_wait(&s.w_full, (w_uses - 1) & 1u, p.status);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       Ring r;
-      const uint32_t idesc = umma_idesc_bf16(kDxH, kDxTok, true, false);
+      const uint32_t idesc = umma_idesc_bf16(256, kDxTok, true, false);
       const uint32_t w0 = smem_u32(w_smem), b0 = smem_u32(ring);
       int cur = -1, w_uses = 0, n = 0;
       bool ok = true;
@@ -420,32 +569,32 @@ __global__ void __launch_bounds__(kDxThreads, 1)
         const int h = (int)(i / t_tiles);
         if (h != cur) {
           cur = h;
-          if (!mbar_wait(&w_full, w_uses & 1u, p.status)) { ok = false; break; }
+          if (!mbar_wait(&s.w_full, w_uses & 1u, p.status)) { ok = false; break; }
           ++w_uses;
         }
         const int buf = n & 1;
-        if (!mbar_wait(&acc_empty[buf], ((n >> 1) & 1u) ^ 1u, p.status)) { ok = false; break; }
+        if (!mbar_wait(&s.acc_empty[buf], ((n >> 1) & 1u) ^ 1u, p.status)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d = tmem + buf * 256;
         for (int kb = 0; kb < n_kb && ok; ++kb) {
           const int steps = min(4, (p.E - 64 * kb + 15) / 16);
           for (int c = 0; c < 2; ++c) {   // dl's piece: with both pieces of W, then with the first
-            if (!mbar_wait(&full[r.st], r.ph, p.status)) { ok = false; break; }
+            if (!mbar_wait(&s.full[r.st], r.ph, p.status)) { ok = false; break; }
             tc_fence_after();
             const uint64_t bd = umma_desc_sw128(b0 + r.st * kDxStage);
             for (int wc = 0; wc < 2 - c; ++wc) {
               const uint64_t ad = umma_desc_mn_sw128(w0 + (wc * n_kb + kb) * 2 * kDxWBox, kDxWBox);
               for (int ks = 0; ks < steps; ++ks)
-                umma_f16(d, ad + ks * (2048 >> 4), bd + ks * (32 >> 4), idesc,
-                         kb > 0 || c > 0 || wc > 0 || ks > 0 ? 1u : 0u);
+                umma2_f16(d, ad + ks * (2048 >> 4), bd + ks * (32 >> 4), idesc,
+                          kb > 0 || c > 0 || wc > 0 || ks > 0 ? 1u : 0u);
             }
-            umma_commit(&empty[r.st]);
+            umma2_commit(&s.empty[r.st]);
             r.next(p.stages);
           }
         }
         if (!ok) break;
-        umma_commit(&acc_full[buf]);
-        if (i + 1 < i1 && (int)((i + 1) / t_tiles) != cur) umma_commit(&w_empty);
+        umma2_commit(&s.acc_full[buf]);
+        if (i + 1 < i1 && (int)((i + 1) / t_tiles) != cur) umma2_commit(&s.w_empty);
       }
     }
   } else {
@@ -453,14 +602,15 @@ __global__ void __launch_bounds__(kDxThreads, 1)
     // lane 4 consecutive h of one token of every four: 8-byte stores, 64
     // consecutive bytes a token.
     const int qd = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t empty_bar[2] = {cluster_addr(&s.acc_empty[0], 0), cluster_addr(&s.acc_empty[1], 0)};
     int n = 0;
     for (long long i = i0; i < i1; ++i, ++n) {
       const int h = (int)(i / t_tiles), t0 = (int)(i - (long long)h * t_tiles) * kDxTok;
       const int buf = n & 1;
-      const int okw = lane == 0 ? (mbar_wait(&acc_full[buf], (n >> 1) & 1u, p.status) ? 1 : 0) : 0;
-      if (!__shfl_sync(0xffffffffu, okw, 0)) break;
+      if (!warp_wait(&s.acc_full[buf], (n >> 1) & 1u, lane, p.status)) break;
       tc_fence_after();
-      __nv_bfloat16 *out = p.out + (size_t)h * kDxH + 32 * qd + (lane & ~3);
+      const int h0 = h * kTileH + 128 * (int)rank;   // H is a multiple of 128
+      __nv_bfloat16 *out = p.out + h0 + 32 * qd + (lane & ~3);
       for (int c0 = 32 * half; c0 < kDxTok; c0 += 64) {
         float v[32];
         tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * qd) << 16) + buf * 256 + c0, v);
@@ -476,42 +626,49 @@ __global__ void __launch_bounds__(kDxThreads, 1)
           const uint32_t keep = high ? bf162_bits(hi) : bf162_bits(lo);
           const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? bf162_bits(lo) : bf162_bits(hi), 2);
           const int t = t0 + c0 + q + (lane & 3);
-          if (t < p.T)
+          if (t < p.T && h0 < p.H)
             *reinterpret_cast<uint2 *>(out + (size_t)t * p.H) =
                 high ? make_uint2(got, keep) : make_uint2(keep, got);
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      if (lane == 0) cluster_arrive(empty_bar[buf]);
     }
   }
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, kTmem);
-  }
+  pair_end(s, warp);
 }
 
-// dW = sum of its splits, db = sum of the prep blocks' parts, in order.
-__global__ void __launch_bounds__(256) route_grad_sum_kernel(const RouteGradParams p, int splits,
+// dW = sum of the runs' parts, db = sum of the prep blocks' parts, in order.
+__global__ void __launch_bounds__(256) route_grad_sum_kernel(const RouteGradParams p, int pairs,
                                                              int dw_blocks) {
   grid_dependency_wait();
   grid_dependency_launch();
   if ((int)blockIdx.x < dw_blocks) {
-    const size_t n4 = (size_t)p.E * p.H / 4;
-    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n4) return;
-    const float4 *part = reinterpret_cast<const float4 *>(p.dW_part) + i;
-    float4 s = part[0];
-    for (int k = 1; k < splits; ++k) {
-      const float4 v = part[k * n4];
+    // four consecutive h of one expert and tile
+    const int tiles = (p.H + kTileH - 1) / kTileH, n_kb = (p.T + kDwTok - 1) / kDwTok;
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int h4 = (int)(i % (kTileH / 4)) * 4;
+    const long long te = i / (kTileH / 4);
+    const int tile = (int)(te / p.E), e = (int)(te - (long long)tile * p.E);
+    if (tile >= tiles || tile * kTileH + h4 >= p.H) return;
+    // the runs that hold units of this tile (run r starts at units r / pairs)
+    const long long units = (long long)tiles * n_kb, first = (long long)tile * n_kb;
+    const int r0 = (int)(((first + 1) * pairs - 1) / units);
+    const int r1 = (int)(((first + n_kb) * pairs - 1) / units);
+    if (r0 == r1) return;   // one run had the whole tile and wrote it
+    const float *part = p.dW_part + ((size_t)(r0 + tile) * p.E + e) * kTileH + h4;
+    float4 s = *reinterpret_cast<const float4 *>(part);
+#pragma unroll 8
+    for (int r = r0 + 1; r <= r1; ++r) {
+      part += (size_t)p.E * kTileH;
+      const float4 v = *reinterpret_cast<const float4 *>(part);
       s.x += v.x;
       s.y += v.y;
       s.z += v.z;
       s.w += v.w;
     }
-    reinterpret_cast<float4 *>(p.dW)[i] = s;
+    *reinterpret_cast<float4 *>(p.dW + (size_t)e * p.H + tile * kTileH + h4) = s;
     return;
   }
   // db: one warp per expert
@@ -525,20 +682,23 @@ __global__ void __launch_bounds__(256) route_grad_sum_kernel(const RouteGradPara
 }
 
 // ---------------------------------------------------------------- host
-constexpr int kSms = 148;
+constexpr int kPairs = 74;   // 148 multiprocessors
 
 int prep_blocks(int T) {
   const int n = (T + kPrepWarps - 1) / kPrepWarps;
-  return n < 2 * kSms ? n : 2 * kSms;
+  return n < 4 * kPairs ? n : 4 * kPairs;
 }
-int dw_tiles(int H) { return (H + kDwH - 1) / kDwH; }
-// Shares of the tokens: as many as fill the multiprocessors, each of at least
-// one stage.
-int dw_splits(int T, int H) {
-  const int n_kb = (T + kDwTok - 1) / kDwTok;
-  int s = kSms / dw_tiles(H);
-  if (s < 1) s = 1;
-  return s < n_kb ? s : n_kb;
+int h_tiles(int H) { return (H + kTileH - 1) / kTileH; }
+// Pairs of blocks for dW: all of them, unless that leaves a run fewer than four
+// stages; then one per tile or a whole number per tile (every part of a tile
+// costs a write and a read of 256 rows).
+int dw_pairs(int T, int H) {
+  const int tiles = h_tiles(H), n_kb = (T + kDwTok - 1) / kDwTok;
+  const long long units = (long long)tiles * n_kb;
+  if (units >= 4 * kPairs) return kPairs;
+  const int per = n_kb / 4 > 1 ? n_kb / 4 : 1;
+  const int n = tiles * per;
+  return n < kPairs ? n : kPairs;
 }
 
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -557,8 +717,7 @@ Layout layout(int T, int E, int H) {
   L.db = off;
   off += up256((size_t)prep_blocks(T) * E * 4);
   L.dw = off;
-  const int splits = dw_splits(T, H);
-  off += splits > 1 ? up256((size_t)splits * E * H * 4) : 0;
+  off += up256((size_t)(dw_pairs(T, H) + h_tiles(H)) * E * kTileH * 4);
   L.total = off;
   return L;
 }
@@ -590,45 +749,46 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
   p.dlp = p.dW || p.dx ? reinterpret_cast<__nv_bfloat16 *>(w + L.dlp) : nullptr;
   p.Wp = reinterpret_cast<__nv_bfloat16 *>(w + L.wp);
   p.db_part = p.db ? reinterpret_cast<float *>(w + L.db) : nullptr;
-  const int splits = dw_splits(p.T, p.H);
-  p.dW_part = splits > 1 ? reinterpret_cast<float *>(w + L.dw) : p.dW;
+  p.dW_part = reinterpret_cast<float *>(w + L.dw);
   const size_t n8 = (size_t)p.E * p.H / 8;
-  const int w_blocks = p.dx ? (int)std::min<size_t>((n8 + 255) / 256, 4 * kSms) : 0;
+  const int w_blocks =
+      p.dx ? (int)std::min<size_t>((n8 + 32 * kPrepWarps - 1) / (32 * kPrepWarps), 4 * kPairs) : 0;
   cudaError_t e = launch_pdl(route_grad_prep_kernel, dim3(p.tok_blocks + w_blocks),
                              dim3(32 * kPrepWarps), 0, stream, p);
-  const int nb = (p.E + 63) / 64;
+  const int pairs = dw_pairs(p.T, p.H), tiles = h_tiles(p.H);
   if (e == cudaSuccess && p.dW) {
     CUtensorMap mx, md;
     if (!encode_planes(&mx, p.x, p.H, p.T, p.H, 1, kDwTok) ||
         !encode_planes(&md, p.dlp, p.E, p.T, p.Epad, 3, kDwTok))
       return cudaErrorInvalidValue;
-    const int stage = (kDwH / 64 + 3 * nb) * kDwBox;
-    DwParams d{p.T, p.H, p.E, splits, std::min(kMaxStages, (kSmemLimit - 2048) / stage), p.dW_part,
+    const int boxes = p.E > 128 ? 2 : 1, stage = (2 + 3 * boxes) * kDwBox;
+    DwParams d{p.T, p.H, p.E, pairs, std::min(kMaxStages, (kSmemLimit - 2048) / stage), p.dW, p.dW_part,
                p.status};
     const int smem = d.stages * stage + 1024;
-    e = cudaFuncSetAttribute(route_grad_dw_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    auto kern = boxes == 2 ? route_grad_dw_kernel<2> : route_grad_dw_kernel<1>;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
-      e = launch_pdl(route_grad_dw_kernel, dim3(dw_tiles(p.H), splits), dim3(kDwThreads), smem, stream,
-                     d, mx, md);
+      e = launch_pdl_cluster(kern, dim3(2 * pairs), 2, dim3(kTcThreads), smem, stream, d, mx, md);
   }
   if (e == cudaSuccess && p.dx) {
     CUtensorMap md, mw;
-    if (!encode_planes(&md, p.dlp, p.E, p.T, p.Epad, 3, kDxTok) ||
+    if (!encode_planes(&md, p.dlp, p.E, p.T, p.Epad, 3, kDxTok / 2) ||
         !encode_planes(&mw, p.Wp, p.H, p.E, p.H, 2, 64))
       return cudaErrorInvalidValue;
-    const int wb = 2 * nb * 2 * kDxWBox;
+    const int wb = 2 * ((p.E + 63) / 64) * 2 * kDxWBox;
     DxParams d{p.T, p.H, p.E, std::min(kMaxStages, (kSmemLimit - 2048 - wb) / kDxStage), p.dx, p.status};
     const int smem = wb + d.stages * kDxStage + 1024;
-    const long long items = (long long)((p.T + kDxTok - 1) / kDxTok) * (p.H / kDxH);
+    const long long items = (long long)((p.T + kDxTok - 1) / kDxTok) * tiles;
     e = cudaFuncSetAttribute(route_grad_dx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
-      e = launch_pdl(route_grad_dx_kernel, dim3((unsigned)std::min<long long>(items, kSms)),
-                     dim3(kDxThreads), smem, stream, d, md, mw);
+      e = launch_pdl_cluster(route_grad_dx_kernel, dim3(2 * (unsigned)std::min<long long>(items, kPairs)),
+                             2, dim3(kTcThreads), smem, stream, d, md, mw);
   }
-  const int dw_blocks = p.dW && splits > 1 ? (int)(((size_t)p.E * p.H / 4 + 255) / 256) : 0;
+  const int dw_blocks =
+      p.dW && tiles % pairs != 0 ? (int)(((long long)tiles * p.E * (kTileH / 4) + 255) / 256) : 0;
   const int db_blocks = p.db ? (p.E + 7) / 8 : 0;
   if (e == cudaSuccess && dw_blocks + db_blocks > 0)
-    e = launch_pdl(route_grad_sum_kernel, dim3(dw_blocks + db_blocks), dim3(256), 0, stream, p, splits,
+    e = launch_pdl(route_grad_sum_kernel, dim3(dw_blocks + db_blocks), dim3(256), 0, stream, p, pairs,
                    dw_blocks);
   return e;
 }
