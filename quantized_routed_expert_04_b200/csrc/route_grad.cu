@@ -197,21 +197,29 @@ __device__ __forceinline__ uint32_t umma_idesc_bf16(int M, int N, bool a_mn, boo
   return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
+// The MMA warp runs its loop as a whole and one elected lane (always the same)
+// issues: control flow and descriptors stay uniform, so that they live in
+// uniform registers as the instruction wants them.  With a loop under
+// `lane == 0` issuing took longer than the 128 cycles that the MMA itself takes
+// (dx: 162-190 cycles each).
 __device__ __forceinline__ void umma2_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                           uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // Arrive on the barrier at this place in both blocks once all earlier MMAs of
-// this thread have completed.
+// the elected lane have completed.
 __device__ __forceinline__ void umma2_commit(uint64_t *bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-      "[%0], %1;" ::"r"(smem_u32(bar)),
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;\n\t}" ::"r"(smem_u32(bar)),
       "h"((uint16_t)3)
       : "memory");
 }
@@ -323,8 +331,10 @@ __device__ __forceinline__ void pair_end(PairShared &s, int warp) {
                  : "memory");
   }
 }
-// One lane waits, the warp learns the outcome.
+// Every lane tests the barrier and the warp votes; only if the phase is not
+// complete yet does one lane wait, within its limit, and tell the others.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int lane, int *status) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const int ok = lane == 0 ? (mbar_wait(bar, parity, status) ? 1 : 0) : 0;
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
@@ -406,7 +416,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           (void)mbar_wait(&s.full[m % p.stages], (uint32_t)(m / p.stages) & 1u, p.status);
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       Ring r;
       const uint32_t idesc = umma_idesc_bf16(256, 128 * kBoxes, true, true);
       int n = 0;   // chains
@@ -415,12 +425,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int tile = (int)(u / n_kb);
         const long long end = min(min(u1, (long long)(tile + 1) * n_kb), u + kDwChain);
         const int buf = n & 1;
-        if (!mbar_wait(&s.acc_empty[buf], ((n >> 1) & 1u) ^ 1u, p.status)) break;
+        if (!warp_wait(&s.acc_empty[buf], ((n >> 1) & 1u) ^ 1u, lane, p.status)) break;
         tc_fence_after();
         const uint32_t d = tmem + buf * 256;
         uint32_t more = 0u;
         for (; u < end; ++u) {
-          if (!mbar_wait(&s.full[r.st], r.ph, p.status)) { ok = false; break; }
+          if (!warp_wait(&s.full[r.st], r.ph, lane, p.status)) { ok = false; break; }
           tc_fence_after();
           const uint32_t a = smem_u32(smem + r.st * kStage);
           const uint64_t ad = umma_desc_mn_sw128(a, kDwBox);
@@ -559,34 +569,43 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       Ring r;
       const uint32_t idesc = umma_idesc_bf16(256, kDxTok, true, false);
-      const uint32_t w0 = smem_u32(w_smem), b0 = smem_u32(ring);
+      const uint64_t ad0 = umma_desc_mn_sw128(smem_u32(w_smem), kDxWBox);
+      const uint64_t bd0 = umma_desc_sw128(smem_u32(ring));
+      const uint32_t w_piece = n_kb * 2 * kDxWBox >> 4;   // W's second piece
       int cur = -1, w_uses = 0, n = 0;
       bool ok = true;
       for (long long i = i0; i < i1 && ok; ++i, ++n) {
         const int h = (int)(i / t_tiles);
         if (h != cur) {
           cur = h;
-          if (!mbar_wait(&s.w_full, w_uses & 1u, p.status)) { ok = false; break; }
+          if (!warp_wait(&s.w_full, w_uses & 1u, lane, p.status)) { ok = false; break; }
           ++w_uses;
         }
         const int buf = n & 1;
-        if (!mbar_wait(&s.acc_empty[buf], ((n >> 1) & 1u) ^ 1u, p.status)) { ok = false; break; }
+        if (!warp_wait(&s.acc_empty[buf], ((n >> 1) & 1u) ^ 1u, lane, p.status)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d = tmem + buf * 256;
+        uint32_t more = 0u;
         for (int kb = 0; kb < n_kb && ok; ++kb) {
           const int steps = min(4, (p.E - 64 * kb + 15) / 16);
-          for (int c = 0; c < 2; ++c) {   // dl's piece: with both pieces of W, then with the first
-            if (!mbar_wait(&s.full[r.st], r.ph, p.status)) { ok = false; break; }
+          // dl's piece c: with both pieces of W, then with the first
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if (!warp_wait(&s.full[r.st], r.ph, lane, p.status)) { ok = false; break; }
             tc_fence_after();
-            const uint64_t bd = umma_desc_sw128(b0 + r.st * kDxStage);
+            const uint64_t bd = bd0 + (uint64_t)(r.st * (kDxStage >> 4));
+            const uint64_t ad = ad0 + (uint64_t)(kb * (2 * kDxWBox >> 4));
+#pragma unroll
             for (int wc = 0; wc < 2 - c; ++wc) {
-              const uint64_t ad = umma_desc_mn_sw128(w0 + (wc * n_kb + kb) * 2 * kDxWBox, kDxWBox);
-              for (int ks = 0; ks < steps; ++ks)
-                umma2_f16(d, ad + ks * (2048 >> 4), bd + ks * (32 >> 4), idesc,
-                          kb > 0 || c > 0 || wc > 0 || ks > 0 ? 1u : 0u);
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                if (ks < steps) {
+                  umma2_f16(d, (wc ? ad + w_piece : ad) + ks * (2048 >> 4), bd + ks * (32 >> 4), idesc, more);
+                  more = 1u;
+                }
             }
             umma2_commit(&s.empty[r.st]);
             r.next(p.stages);
