@@ -158,7 +158,9 @@ struct RouteGradParams {
   // set by run_route_grad (workspace)
   int Epad, tok_blocks;
   __nv_bfloat16 *dlp;      // [3][T][Epad] bf16 pieces of dl
-  __nv_bfloat16 *Wp;       // [2][E][H] bf16 pieces of W
+  __half *dl16;            // [T][Epad] dl / t_scale (up to the scale of W16)
+  float *t_scale;          // [T]
+  __half *W16;             // [E][H] W, scaled
   float *db_part;          // [tok_blocks][E]
   float *dW_part;          // parts of dW, [slot][E][256]
 };

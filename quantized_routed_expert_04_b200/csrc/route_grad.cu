@@ -8,16 +8,18 @@
 //                 dl[idx_j] += scale s_j (1 - s_j) / S (dw_j - sum_i s_i / S dw_i)
 //   dW = dl^T x,   db = sum_t dl,   dx = dl W.
 //
-// Four launches: the rows of dl (and W) as bf16 pieces; dW and dx on the
-// tensor cores (tcgen05, accumulators in tensor memory); the sums of dW's and
-// db's parts.
+// Three launches: the operands in 16 bits; dW on the tensor cores (tcgen05,
+// accumulators in tensor memory); dx on the tensor cores, whose spare warps add
+// up the parts of dW and db.
 //
-// fp32 operands on bf16 tensor cores: a number is the sum of its bf16
-// rounding, the bf16 rounding of what is left, and so on; each piece keeps 8
-// more bits.  dW needs fp32 accuracy: x is bf16 already, dl takes three pieces
-// (24 bits), three exact products per element, added in fp32.  dx is rounded to
-// bf16 at the end: dl and W take two pieces each, and hi hi + hi lo + lo hi
-// leaves out 2^-18 of a product.
+// fp32 operands on 16-bit tensor cores.  dW needs fp32 accuracy: x is bf16
+// already, and dl is taken as the sum of three bf16 numbers (its rounding, the
+// rounding of what is left, and again: 24 bits): three exact products per
+// element, added in fp32.  dx is rounded to bf16 (8 bits) at the end: dl and W
+// are rounded once to f16 (11 bits), dl divided by a power of two per token
+// that puts its row's largest magnitude in [1, 2), W times 2^8.  That is a third
+// of the products that two bf16 pieces of each would take.
+
 #include <cuda.h>
 
 #include <algorithm>
@@ -92,9 +94,18 @@ __device__ __forceinline__ void weight_grad(const RouteGradParams &p, int t, int
   id = use ? id : -1;
 }
 
+// Eight floats -> f16.
+__device__ __forceinline__ uint4 pack_f16(const float v[8], float mul) {
+  return make_uint4(h2_bits(__floats2half2_rn(v[0] * mul, v[1] * mul)),
+                    h2_bits(__floats2half2_rn(v[2] * mul, v[3] * mul)),
+                    h2_bits(__floats2half2_rn(v[4] * mul, v[5] * mul)),
+                    h2_bits(__floats2half2_rn(v[6] * mul, v[7] * mul)));
+}
+constexpr float kWScale = 256.0f;
+
 // Blocks 0 .. tok_blocks - 1: rows of dl, one warp per token at a time, each
-// lane 8 consecutive experts, as three bf16 pieces, and the block's share of
-// db.  The blocks behind them: W as two bf16 pieces.
+// lane 8 consecutive experts, as three bf16 pieces and as scaled f16, and the
+// block's share of db.  The blocks behind them: W as f16.
 __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const RouteGradParams p) {
   __shared__ float s_db[kPrepWarps][kMaxExperts];
   grid_dependency_wait();
@@ -103,13 +114,16 @@ __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const 
   if ((int)blockIdx.x >= p.tok_blocks) {
     const size_t n8 = (size_t)E * p.H / 8;
     const size_t step = (size_t)(gridDim.x - p.tok_blocks) * blockDim.x;
+    bool over = false;
     for (size_t i = (size_t)(blockIdx.x - p.tok_blocks) * blockDim.x + threadIdx.x; i < n8; i += step) {
       const float4 a = reinterpret_cast<const float4 *>(p.W)[2 * i];
       const float4 b = reinterpret_cast<const float4 *>(p.W)[2 * i + 1];
-      float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      reinterpret_cast<uint4 *>(p.Wp)[i] = take_bf16(v);
-      reinterpret_cast<uint4 *>(p.Wp)[n8 + i] = take_bf16(v);
+      const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) over |= fabsf(v[k]) * kWScale >= kF16Overflow;
+      reinterpret_cast<uint4 *>(p.W16)[i] = pack_f16(v, kWScale);
     }
+    if (over) set_status(p.status, STATUS_RANGE);
     return;
   }
   const bool vec = E % 8 == 0 && (reinterpret_cast<uintptr_t>(p.dlogits) & 15) == 0;
@@ -148,9 +162,21 @@ __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const 
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) db[i] += v[i];
+    const size_t at = (size_t)t * (p.Epad / 8) + lane;
+    if (p.dl16) {
+      // the power of two below the row's largest magnitude (within 2^-126 .. 2^126)
+      float m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+      m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+      const int ex = m == 0.0f ? 0 : min(max((int)(__float_as_uint(m) >> 23) - 127, -126), 126);
+      if (8 * lane < E)
+        reinterpret_cast<uint4 *>(p.dl16)[at] = pack_f16(v, __uint_as_float((uint32_t)(127 - ex) << 23));
+      if (lane == 0) p.t_scale[t] = __uint_as_float((uint32_t)(127 + ex) << 23) * (1.0f / kWScale);
+    }
     if (p.dlp && 8 * lane < E) {
       const size_t plane = (size_t)p.T * p.Epad / 8;
-      uint4 *out = reinterpret_cast<uint4 *>(p.dlp) + (size_t)t * (p.Epad / 8) + lane;
+      uint4 *out = reinterpret_cast<uint4 *>(p.dlp) + at;
       out[0] = take_bf16(v);
       out[plane] = take_bf16(v);
       out[2 * plane] = take_bf16(v);
@@ -192,9 +218,10 @@ __device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t smem_addr, uint3
   d |= (uint64_t)2 << 61;
   return d;
 }
-// bf16 A and B, f32 accumulator; a_mn, b_mn: the operand is MN-major.
-__device__ __forceinline__ uint32_t umma_idesc_bf16(int M, int N, bool a_mn, bool b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+// f32 accumulator, A and B both bf16 or both f16; a_mn, b_mn: the operand is
+// MN-major.
+__device__ __forceinline__ uint32_t umma_idesc_16(bool bf16, int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 // The MMA warp runs its loop as a whole and one elected lane (always the same)
@@ -272,6 +299,16 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, float v[16]) 
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// A tile of this block's shared memory -> global memory; rows and columns
+// outside the tensor are left out.
+__device__ __forceinline__ void tma_store_2d(const void *tmap, const void *src, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(tmap),
+      "r"(c0), "r"(c1), "r"(smem_u32(src))
+      : "memory");
+}
+
 struct Ring {
   uint32_t st = 0, ph = 0;
   __device__ __forceinline__ void next(uint32_t stages) {
@@ -292,7 +329,7 @@ constexpr int kTcThreads = 32 * (2 + kEpiWarps);   // producer, MMA, epilogue
 // Barriers of a block (those that count arrivals of both blocks live in the
 // first one) and the pair's tensor memory.
 struct PairShared {
-  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], w_full, w_empty;
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], w_full[4], w_empty;
   uint32_t tmem;
 };
 
@@ -306,7 +343,7 @@ __device__ __forceinline__ void pair_begin(PairShared &s, int stages, int warp) 
       mbar_init(&s.acc_full[i], 1);
       mbar_init(&s.acc_empty[i], 2 * kEpiWarps);
     }
-    mbar_init(&s.w_full, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&s.w_full[i], 1);
     mbar_init(&s.w_empty, 1);
     fence_mbar_init();
   }
@@ -418,7 +455,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   } else if (warp == 1) {
     if (rank == 0) {
       Ring r;
-      const uint32_t idesc = umma_idesc_bf16(256, 128 * kBoxes, true, true);
+      const uint32_t idesc = umma_idesc_16(true, 256, 128 * kBoxes, true, true);
       int n = 0;   // chains
       bool ok = true;
       for (long long u = u0; u < u1 && ok; ++n) {
@@ -492,25 +529,85 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   pair_end(s, warp);
 }
 
-// dx[t][h] = sum_e dl[t][e] W[e][h]: M = 256 rows of h, N = 256 tokens, K = the
-// experts.  A block's 128 rows of W (both pieces, every expert) stay in shared
-// memory while blocks of 256 tokens of dl stream past it in stages of 64
-// experts of one piece.  Work items (h tile, token tile), h-major, in one
-// contiguous run per pair: W is loaded again only where a run crosses into the
-// next h tile.
+// ---- the last sums: dW from the runs' parts, db from the prep blocks' parts
+struct SumParams {
+  RouteGradParams g;
+  int pairs;          // runs of the dW kernel
+  int dw_quads;       // groups of four h to add up: tiles * E * 64, or 0
+};
+
+// Four consecutive h of one expert and tile.
+__device__ __forceinline__ void sum_dw(const SumParams &q, int i) {
+  const RouteGradParams &p = q.g;
+  const int tiles = (p.H + kTileH - 1) / kTileH, n_kb = (p.T + kDwTok - 1) / kDwTok;
+  const int h4 = i % (kTileH / 4) * 4, te = i / (kTileH / 4);
+  const int tile = te / p.E, e = te - tile * p.E;
+  if (tile * kTileH + h4 >= p.H) return;
+  // the runs that hold units of this tile (run r starts at unit units r / pairs)
+  const long long units = (long long)tiles * n_kb, first = (long long)tile * n_kb;
+  const int r0 = (int)(((first + 1) * q.pairs - 1) / units);
+  const int r1 = (int)(((first + n_kb) * q.pairs - 1) / units);
+  if (r0 == r1) return;   // one run had the whole tile and wrote it
+  const float *part = p.dW_part + ((size_t)(r0 + tile) * p.E + e) * kTileH + h4;
+  float4 s = __ldcg(reinterpret_cast<const float4 *>(part));
+#pragma unroll 4
+  for (int r = r0 + 1; r <= r1; ++r) {
+    part += (size_t)p.E * kTileH;
+    const float4 v = __ldcg(reinterpret_cast<const float4 *>(part));
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  }
+  *reinterpret_cast<float4 *>(p.dW + (size_t)e * p.H + tile * kTileH + h4) = s;
+}
+// One warp: expert e.
+__device__ __forceinline__ void sum_db(const RouteGradParams &p, int e, int lane) {
+  double s = 0.0;
+#pragma unroll 4
+  for (int b = lane; b < p.tok_blocks; b += 32) s += __ldcg(p.db_part + (size_t)b * p.E + e);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) p.db[e] = (float)s;
+}
+// The whole of it, by warp `warp` of `warps`.
+__device__ __forceinline__ void sum_parts(const SumParams &q, int warp, int warps, int lane) {
+  if (q.g.db)
+    for (int e = warp; e < q.g.E; e += warps) sum_db(q.g, e, lane);
+#pragma unroll 2
+  for (int i = warp * 32 + lane; i < q.dw_quads; i += warps * 32) sum_dw(q, i);
+}
+// ... in a launch of its own, where dx is not wanted.
+__global__ void __launch_bounds__(256) route_grad_sum_kernel(const SumParams q) {
+  grid_dependency_wait();
+  grid_dependency_launch();
+  sum_parts(q, blockIdx.x * 8 + (threadIdx.x >> 5), gridDim.x * 8, threadIdx.x & 31);
+}
+
+// dx[t][h] = sum_e dl[t][e] W[e][h]: M = 256 tokens, N = 256 rows of h, K = the
+// experts, in f16.  W's share of the tile (every expert) stays in shared memory
+// while tokens stream past it in stages of 64 experts.  Work items (h tile,
+// token tile), h-major, in one contiguous run per pair: W is loaded again only
+// where a run crosses into the next h tile.  The product itself is 16 MMAs an
+// item (2048 cycles with 256 experts), so writing dx counts: each lane scales
+// its token's row, writes bf16 to a swizzled tile, and bulk stores take it out.
 constexpr int kDxTok = 256;
 constexpr int kDxStage = kDxTok / 2 * 128;   // per block
 constexpr int kDxWBox = 64 * 128;
+constexpr int kDxOut = 32 * 128;             // 32 tokens x 64 h of bf16
+constexpr int kSumWarps = 4;
+constexpr int kDxThreads = kTcThreads + 32 * kSumWarps;
 
 struct DxParams {
   int T, H, E, stages;
-  __nv_bfloat16 *out;   // [T][H]
+  const float *t_scale;   // [T]
   int *status;
 };
 
-__global__ void __launch_bounds__(kTcThreads, 1)
-    route_grad_dx_kernel(const DxParams p, const __grid_constant__ CUtensorMap map_dl,
-                         const __grid_constant__ CUtensorMap map_w) {
+__global__ void __launch_bounds__(kDxThreads, 1)
+    route_grad_dx_kernel(const DxParams p, const SumParams q, const __grid_constant__ CUtensorMap map_dl,
+                         const __grid_constant__ CUtensorMap map_w,
+                         const __grid_constant__ CUtensorMap map_dx) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ PairShared s;
   uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -519,6 +616,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (threadIdx.x == 0) {
     prefetch_tmap(&map_dl);
     prefetch_tmap(&map_w);
+    prefetch_tmap(&map_dx);
   }
   pair_begin(s, p.stages, warp);
   const uint32_t tmem = s.tmem, rank = cluster_rank();
@@ -530,9 +628,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const long long items = (long long)t_tiles * ((p.H + kTileH - 1) / kTileH);
   const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
   const long long i0 = run_begin(items, pairs, pair), i1 = run_begin(items, pairs, pair + 1);
-  const uint32_t w_bytes = 2 * n_kb * 2 * kDxWBox;
-  uint8_t *w_smem = smem;                              // [piece][k block][h half]
-  uint8_t *ring = smem + w_bytes;
+  uint8_t *w_smem = smem;                              // [k block][half of the block's 128 h]
+  uint8_t *ring = smem + n_kb * 2 * kDxWBox;
+  uint8_t *out_smem = ring + p.stages * kDxStage;      // [epilogue warp][2]
   if (warp == 0) {
     if (lane == 0) {
       Ring r;
@@ -541,163 +639,124 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       bool ok = true;
       for (long long i = i0; i < i1 && ok; ++i) {
         const int h = (int)(i / t_tiles), t = (int)(i - (long long)h * t_tiles);
-        if (h != cur) {
+        const bool fresh = h != cur;
+        if (fresh) {
           if (cur >= 0 && !mbar_wait(&s.w_empty, (w_uses - 1) & 1u, p.status)) { ok = false; break; }
           cur = h;
           ++w_uses;
-          const uint32_t bar = cluster_addr(&s.w_full, 0);
-          if (rank == 0) mbar_arrive_expect_tx(&s.w_full, 2 * w_bytes);
-          for (int c = 0; c < 2; ++c)
-            for (int kb = 0; kb < n_kb; ++kb)
-              for (int m = 0; m < 2; ++m)
-                tma2_load_3d(w_smem + ((c * n_kb + kb) * 2 + m) * kDxWBox, &map_w,
-                             h * kTileH + 128 * (int)rank + 64 * m, 64 * kb, c, bar);
         }
-        for (int q = 0; q < 2 * n_kb; ++q) {
-          if (!mbar_wait(&s.empty[r.st], r.ph ^ 1u, p.status)) { ok = false; break; }
+        for (int kb = 0; kb < n_kb; ++kb) {
+          if (fresh) {
+            const uint32_t bar = cluster_addr(&s.w_full[kb], 0);
+            if (rank == 0) mbar_arrive_expect_tx(&s.w_full[kb], 4 * kDxWBox);
+            for (int m = 0; m < 2; ++m)
+              tma2_load_2d(w_smem + (kb * 2 + m) * kDxWBox, &map_w, h * kTileH + 128 * (int)rank + 64 * m,
+                           64 * kb, bar);
+          }
+          if (ok && !mbar_wait(&s.empty[r.st], r.ph ^ 1u, p.status)) ok = false;
+          if (!ok) continue;   // (every copy of W that a barrier expects is still issued)
           if (rank == 0) mbar_arrive_expect_tx(&s.full[r.st], 2 * kDxStage);
-          tma2_load_3d(ring + r.st * kDxStage, &map_dl, 64 * (q >> 1), t * kDxTok + kDxTok / 2 * (int)rank,
-                       q & 1, cluster_addr(&s.full[r.st], 0));
+          tma2_load_2d(ring + r.st * kDxStage, &map_dl, 64 * kb, t * kDxTok + kDxTok / 2 * (int)rank,
+                       cluster_addr(&s.full[r.st], 0));
           ++issued;
           r.next(p.stages);
         }
       }
-      if (!ok && rank == 0) {
+      if (!ok && rank == 0) {   // let issued copies land
         for (long long m = issued > p.stages ? issued - p.stages : 0; m < issued; ++m)
           (void)mbar_wait(&s.full[m % p.stages], (uint32_t)(m / p.stages) & 1u, p.status);
-        if (w_uses) (void)mbar_wait(&s.w_full, (w_uses - 1) & 1u, p.status);
+        for (int kb = 0; w_uses && kb < n_kb; ++kb) (void)mbar_wait(&s.w_full[kb], (w_uses - 1) & 1u, p.status);
       }
     }
   } else if (warp == 1) {
     if (rank == 0) {
       Ring r;
-      const uint32_t idesc = umma_idesc_bf16(256, kDxTok, true, false);
-      const uint64_t ad0 = umma_desc_mn_sw128(smem_u32(w_smem), kDxWBox);
-      const uint64_t bd0 = umma_desc_sw128(smem_u32(ring));
-      const uint32_t w_piece = n_kb * 2 * kDxWBox >> 4;   // W's second piece
+      const uint32_t idesc = umma_idesc_16(false, kDxTok, kTileH, false, true);
+      const uint64_t bd0 = umma_desc_mn_sw128(smem_u32(w_smem), kDxWBox);
+      const uint64_t ad0 = umma_desc_sw128(smem_u32(ring));
       int cur = -1, w_uses = 0, n = 0;
       bool ok = true;
       for (long long i = i0; i < i1 && ok; ++i, ++n) {
         const int h = (int)(i / t_tiles);
-        if (h != cur) {
+        const bool fresh = h != cur;
+        if (fresh) {
           cur = h;
-          if (!warp_wait(&s.w_full, w_uses & 1u, lane, p.status)) { ok = false; break; }
           ++w_uses;
         }
         const int buf = n & 1;
         if (!warp_wait(&s.acc_empty[buf], ((n >> 1) & 1u) ^ 1u, lane, p.status)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d = tmem + buf * 256;
-        uint32_t more = 0u;
-        for (int kb = 0; kb < n_kb && ok; ++kb) {
+        for (int kb = 0; kb < n_kb; ++kb) {
+          if ((fresh && !warp_wait(&s.w_full[kb], (w_uses - 1) & 1u, lane, p.status)) ||
+              !warp_wait(&s.full[r.st], r.ph, lane, p.status)) { ok = false; break; }
+          tc_fence_after();
           const int steps = min(4, (p.E - 64 * kb + 15) / 16);
-          // dl's piece c: with both pieces of W, then with the first
+          const uint64_t ad = ad0 + (uint64_t)(r.st * (kDxStage >> 4));
+          const uint64_t bd = bd0 + (uint64_t)(kb * (2 * kDxWBox >> 4));
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            if (!warp_wait(&s.full[r.st], r.ph, lane, p.status)) { ok = false; break; }
-            tc_fence_after();
-            const uint64_t bd = bd0 + (uint64_t)(r.st * (kDxStage >> 4));
-            const uint64_t ad = ad0 + (uint64_t)(kb * (2 * kDxWBox >> 4));
-#pragma unroll
-            for (int wc = 0; wc < 2 - c; ++wc) {
-#pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                if (ks < steps) {
-                  umma2_f16(d, (wc ? ad + w_piece : ad) + ks * (2048 >> 4), bd + ks * (32 >> 4), idesc, more);
-                  more = 1u;
-                }
-            }
-            umma2_commit(&s.empty[r.st]);
-            r.next(p.stages);
-          }
+          for (int ks = 0; ks < 4; ++ks)
+            if (ks < steps)
+              umma2_f16(d, ad + ks * (32 >> 4), bd + ks * (2048 >> 4), idesc, kb > 0 || ks > 0 ? 1u : 0u);
+          umma2_commit(&s.empty[r.st]);
+          r.next(p.stages);
         }
         if (!ok) break;
         umma2_commit(&s.acc_full[buf]);
         if (i + 1 < i1 && (int)((i + 1) / t_tiles) != cur) umma2_commit(&s.w_empty);
       }
     }
-  } else {
-    // lane: one h; column: one token.  Two steps of pairwise exchange give each
-    // lane 4 consecutive h of one token of every four: 8-byte stores, 64
-    // consecutive bytes a token.
+  } else if (warp < 2 + kEpiWarps) {
+    // lane: one token; column: one h.  Each warp: a quarter of the block's 128
+    // tokens and half of the columns, 64 at a time.
     const int qd = warp & 3, half = (warp - 2) >> 2;
     const uint32_t empty_bar[2] = {cluster_addr(&s.acc_empty[0], 0), cluster_addr(&s.acc_empty[1], 0)};
+    uint8_t *tile = out_smem + (warp - 2) * 2 * kDxOut;
     int n = 0;
     for (long long i = i0; i < i1; ++i, ++n) {
       const int h = (int)(i / t_tiles), t0 = (int)(i - (long long)h * t_tiles) * kDxTok;
+      const int tok0 = t0 + kDxTok / 2 * (int)rank + 32 * qd;
+      const float scale = tok0 + lane < p.T ? p.t_scale[tok0 + lane] : 0.0f;
       const int buf = n & 1;
       if (!warp_wait(&s.acc_full[buf], (n >> 1) & 1u, lane, p.status)) break;
       tc_fence_after();
-      const int h0 = h * kTileH + 128 * (int)rank;   // H is a multiple of 128
-      __nv_bfloat16 *out = p.out + h0 + 32 * qd + (lane & ~3);
-      for (int c0 = 32 * half; c0 < kDxTok; c0 += 64) {
-        float v[32];
-        tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * qd) << 16) + buf * 256 + c0, v);
 #pragma unroll
-        for (int q = 0; q < 32; q += 4) {
-          // lanes 4 l + s, columns q + s: transpose 4 x 4
-          const bool odd = lane & 1, high = lane & 2;
-          const float a = __shfl_xor_sync(0xffffffffu, odd ? v[q] : v[q + 1], 1);
-          const float b = __shfl_xor_sync(0xffffffffu, odd ? v[q + 2] : v[q + 3], 1);
-          // column q (even lanes) or q + 1 (odd): this pair of h; the same for q + 2, q + 3
-          const __nv_bfloat162 lo = odd ? __floats2bfloat162_rn(a, v[q + 1]) : __floats2bfloat162_rn(v[q], a);
-          const __nv_bfloat162 hi = odd ? __floats2bfloat162_rn(b, v[q + 3]) : __floats2bfloat162_rn(v[q + 2], b);
-          const uint32_t keep = high ? bf162_bits(hi) : bf162_bits(lo);
-          const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? bf162_bits(lo) : bf162_bits(hi), 2);
-          const int t = t0 + c0 + q + (lane & 3);
-          if (t < p.T && h0 < p.H)
-            *reinterpret_cast<uint2 *>(out + (size_t)t * p.H) =
-                high ? make_uint2(got, keep) : make_uint2(keep, got);
+      for (int b = 0; b < 2; ++b) {
+        const int col = 128 * half + 64 * b;
+        uint32_t o[32];
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+          float v[32];
+          tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * qd) << 16) + buf * 256 + col + c, v);
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            o[c / 2 + k] = bf162_bits(__floats2bfloat162_rn(v[2 * k] * scale, v[2 * k + 1] * scale));
         }
+        if (b == 1) {   // the accumulator is in registers
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) cluster_arrive(empty_bar[buf]);
+        }
+        // the tile's last store has read it
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        __syncwarp();
+        uint8_t *dst = tile + b * kDxOut + lane * 128;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<uint4 *>(dst + ((k ^ (lane & 7)) << 4)) =
+              make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        fence_async_smem();
+        __syncwarp();
+        const int h0 = h * kTileH + col;   // H is a multiple of 128
+        if (lane == 0 && h0 < p.H && tok0 < p.T) tma_store_2d(&map_dx, tile + b * kDxOut, h0, tok0);
+        __syncwarp();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) cluster_arrive(empty_bar[buf]);
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  } else {
+    sum_parts(q, blockIdx.x * kSumWarps + warp - 2 - kEpiWarps, gridDim.x * kSumWarps, lane);
   }
   pair_end(s, warp);
-}
-
-// dW = sum of the runs' parts, db = sum of the prep blocks' parts, in order.
-__global__ void __launch_bounds__(256) route_grad_sum_kernel(const RouteGradParams p, int pairs,
-                                                             int dw_blocks) {
-  grid_dependency_wait();
-  grid_dependency_launch();
-  if ((int)blockIdx.x < dw_blocks) {
-    // four consecutive h of one expert and tile
-    const int tiles = (p.H + kTileH - 1) / kTileH, n_kb = (p.T + kDwTok - 1) / kDwTok;
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    const int h4 = (int)(i % (kTileH / 4)) * 4;
-    const long long te = i / (kTileH / 4);
-    const int tile = (int)(te / p.E), e = (int)(te - (long long)tile * p.E);
-    if (tile >= tiles || tile * kTileH + h4 >= p.H) return;
-    // the runs that hold units of this tile (run r starts at units r / pairs)
-    const long long units = (long long)tiles * n_kb, first = (long long)tile * n_kb;
-    const int r0 = (int)(((first + 1) * pairs - 1) / units);
-    const int r1 = (int)(((first + n_kb) * pairs - 1) / units);
-    if (r0 == r1) return;   // one run had the whole tile and wrote it
-    const float *part = p.dW_part + ((size_t)(r0 + tile) * p.E + e) * kTileH + h4;
-    float4 s = *reinterpret_cast<const float4 *>(part);
-#pragma unroll 8
-    for (int r = r0 + 1; r <= r1; ++r) {
-      part += (size_t)p.E * kTileH;
-      const float4 v = *reinterpret_cast<const float4 *>(part);
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
-    }
-    *reinterpret_cast<float4 *>(p.dW + (size_t)e * p.H + tile * kTileH + h4) = s;
-    return;
-  }
-  // db: one warp per expert
-  const int e = (blockIdx.x - dw_blocks) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (e >= p.E) return;
-  double s = 0.0;
-  for (int b = lane; b < p.tok_blocks; b += 32) s += p.db_part[(size_t)b * p.E + e];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) p.db[e] = (float)s;
 }
 
 // ---------------------------------------------------------------- host
@@ -723,7 +782,7 @@ int dw_pairs(int T, int H) {
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct Layout {
-  size_t dlp, wp, db, dw, total;
+  size_t dlp, dl16, t_scale, w16, db, dw, total;
 };
 Layout layout(int T, int E, int H) {
   const int Epad = (E + 7) / 8 * 8;
@@ -731,8 +790,12 @@ Layout layout(int T, int E, int H) {
   size_t off = 0;
   L.dlp = off;
   off += up256((size_t)3 * T * Epad * 2);
-  L.wp = off;
-  off += up256((size_t)2 * E * H * 2);
+  L.dl16 = off;
+  off += up256((size_t)T * Epad * 2);
+  L.t_scale = off;
+  off += up256((size_t)T * 4);
+  L.w16 = off;
+  off += up256((size_t)E * H * 2);
   L.db = off;
   off += up256((size_t)prep_blocks(T) * E * 4);
   L.dw = off;
@@ -741,9 +804,9 @@ Layout layout(int T, int E, int H) {
   return L;
 }
 
-// bf16 [planes][rows][cols], row stride ld elements, as boxes of 64 x box_rows
-// (one plane), 128-byte swizzle; elements outside read as zero.
-bool encode_planes(CUtensorMap *m, const void *base, int cols, int rows, int ld, int planes,
+// 16-bit elements [planes][rows][cols], row stride ld elements, as boxes of 64 x
+// box_rows (one plane), 128-byte swizzle; elements outside read as zero.
+bool encode_planes(CUtensorMap *m, CUtensorMapDataType type, const void *base, int cols, int rows, int ld, int planes,
                    int box_rows) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
@@ -751,7 +814,7 @@ bool encode_planes(CUtensorMap *m, const void *base, int cols, int rows, int ld,
   cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * rows};
   cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes > 1 ? 3 : 2, const_cast<void *>(base), dims,
+  return enc(m, type, planes > 1 ? 3 : 2, const_cast<void *>(base), dims,
              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -765,8 +828,10 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
   char *w = static_cast<char *>(workspace);
   p.Epad = (p.E + 7) / 8 * 8;
   p.tok_blocks = prep_blocks(p.T);
-  p.dlp = p.dW || p.dx ? reinterpret_cast<__nv_bfloat16 *>(w + L.dlp) : nullptr;
-  p.Wp = reinterpret_cast<__nv_bfloat16 *>(w + L.wp);
+  p.dlp = p.dW ? reinterpret_cast<__nv_bfloat16 *>(w + L.dlp) : nullptr;
+  p.dl16 = p.dx ? reinterpret_cast<__half *>(w + L.dl16) : nullptr;
+  p.t_scale = reinterpret_cast<float *>(w + L.t_scale);
+  p.W16 = reinterpret_cast<__half *>(w + L.w16);
   p.db_part = p.db ? reinterpret_cast<float *>(w + L.db) : nullptr;
   p.dW_part = reinterpret_cast<float *>(w + L.dw);
   const size_t n8 = (size_t)p.E * p.H / 8;
@@ -774,11 +839,12 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
       p.dx ? (int)std::min<size_t>((n8 + 32 * kPrepWarps - 1) / (32 * kPrepWarps), 4 * kPairs) : 0;
   cudaError_t e = launch_pdl(route_grad_prep_kernel, dim3(p.tok_blocks + w_blocks),
                              dim3(32 * kPrepWarps), 0, stream, p);
+  const auto kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kF16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const int pairs = dw_pairs(p.T, p.H), tiles = h_tiles(p.H);
   if (e == cudaSuccess && p.dW) {
     CUtensorMap mx, md;
-    if (!encode_planes(&mx, p.x, p.H, p.T, p.H, 1, kDwTok) ||
-        !encode_planes(&md, p.dlp, p.E, p.T, p.Epad, 3, kDwTok))
+    if (!encode_planes(&mx, kBf16, p.x, p.H, p.T, p.H, 1, kDwTok) ||
+        !encode_planes(&md, kBf16, p.dlp, p.E, p.T, p.Epad, 3, kDwTok))
       return cudaErrorInvalidValue;
     const int boxes = p.E > 128 ? 2 : 1, stage = (2 + 3 * boxes) * kDwBox;
     DwParams d{p.T, p.H, p.E, pairs, std::min(kMaxStages, (kSmemLimit - 2048) / stage), p.dW, p.dW_part,
@@ -789,26 +855,26 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
     if (e == cudaSuccess)
       e = launch_pdl_cluster(kern, dim3(2 * pairs), 2, dim3(kTcThreads), smem, stream, d, mx, md);
   }
+  const SumParams q{p, pairs, p.dW && tiles % pairs != 0 ? tiles * p.E * (kTileH / 4) : 0};
   if (e == cudaSuccess && p.dx) {
-    CUtensorMap md, mw;
-    if (!encode_planes(&md, p.dlp, p.E, p.T, p.Epad, 3, kDxTok / 2) ||
-        !encode_planes(&mw, p.Wp, p.H, p.E, p.H, 2, 64))
+    CUtensorMap md, mw, mo;
+    if (!encode_planes(&md, kF16, p.dl16, p.E, p.T, p.Epad, 1, kDxTok / 2) ||
+        !encode_planes(&mw, kF16, p.W16, p.H, p.E, p.H, 1, 64) ||
+        !encode_planes(&mo, kBf16, p.dx, p.H, p.T, p.H, 1, 32))
       return cudaErrorInvalidValue;
-    const int wb = 2 * ((p.E + 63) / 64) * 2 * kDxWBox;
-    DxParams d{p.T, p.H, p.E, std::min(kMaxStages, (kSmemLimit - 2048 - wb) / kDxStage), p.dx, p.status};
-    const int smem = wb + d.stages * kDxStage + 1024;
+    const int fixed = (p.E + 63) / 64 * 2 * kDxWBox + kEpiWarps * 2 * kDxOut;
+    DxParams d{p.T, p.H, p.E, std::min(kMaxStages, (kSmemLimit - 2048 - fixed) / kDxStage), p.t_scale,
+               p.status};
+    const int smem = fixed + d.stages * kDxStage + 1024;
     const long long items = (long long)((p.T + kDxTok - 1) / kDxTok) * tiles;
     e = cudaFuncSetAttribute(route_grad_dx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
       e = launch_pdl_cluster(route_grad_dx_kernel, dim3(2 * (unsigned)std::min<long long>(items, kPairs)),
-                             2, dim3(kTcThreads), smem, stream, d, md, mw);
+                             2, dim3(kDxThreads), smem, stream, d, q, md, mw, mo);
+  } else if (e == cudaSuccess && (p.db || q.dw_quads)) {
+    const int blocks = std::max((p.E + 7) / 8, (q.dw_quads + 255) / 256);
+    e = launch_pdl(route_grad_sum_kernel, dim3(blocks), dim3(256), 0, stream, q);
   }
-  const int dw_blocks =
-      p.dW && tiles % pairs != 0 ? (int)(((long long)tiles * p.E * (kTileH / 4) + 255) / 256) : 0;
-  const int db_blocks = p.db ? (p.E + 7) / 8 : 0;
-  if (e == cudaSuccess && dw_blocks + db_blocks > 0)
-    e = launch_pdl(route_grad_sum_kernel, dim3(dw_blocks + db_blocks), dim3(256), 0, stream, p, pairs,
-                   dw_blocks);
   return e;
 }
 

@@ -10,9 +10,10 @@ dW: dl carries 32 u of the sum of its terms' magnitudes; its products with x
 are exact to u (dl as a sum of three bf16 numbers keeps 24 bits); the tensor
 core adds 16 of them at a time and may cut the running sum at 2^-23, three
 times per 16 tokens: (3 T / 8 + 64) u of sum |dl| |x|.
-dx: dl and W as sums of two bf16 numbers each, 2^-18 relative, the product of
-the two low parts left out (2^-18): within 2^-16 of sum |dl| |W|, then half a
-bf16 step, 2^-8.
+dx: dl and W rounded once to f16, half a step each: 2^-11 relative, so 2^-10
+(1 + 2^-10) of sum |dl| |W|; below f16's normal range half a step is absolute:
+2^-25 of the row's power of two for dl, 2^-25 / 2^8 for W.  Then half a bf16
+step, 2^-8.
 """
 import math
 
@@ -336,6 +337,13 @@ def run_route_backward(layer, x, logits, idx, dw, dlogits, want=("dW", "db", "dx
     return out
 
 
+def dx_rounding(dl, W):
+    """The bound on what rounding dl and W to f16 changes in dl W."""
+    a, w = dl.abs(), W.double().abs()
+    return (a @ w) * 2.0 ** -10 * (1 + 2.0 ** -9) + \
+        (a.amax(1, keepdim=True) * w.sum(0)) * 2.0 ** -25 + a.sum(1, keepdim=True) * 2.0 ** -33
+
+
 def check_route_backward(layer, x, W, logits, idx, dw, dlogits, mode, **kw):
     T = x.shape[0]
     out = run_route_backward(layer, x, logits, idx, dw, dlogits, **kw)
@@ -356,8 +364,7 @@ def check_route_backward(layer, x, W, logits, idx, dw, dlogits, mode, **kw):
         assert bool((err <= tol + 1e-38).all()), float((err / (tol + 1e-38)).max())
     if "dx" in out:
         want = dl @ W.double()
-        tol = (dl.abs() @ W.double().abs()) * 2.0 ** -16 + (mag @ W.double().abs()) * 32 * U + \
-            want.abs() * 2.0 ** -8
+        tol = dx_rounding(dl, W) + (mag @ W.double().abs()) * 32 * U + want.abs() * 2.0 ** -8
         err = (out["dx"].double() - want).abs()
         assert bool((err <= tol + 1e-38).all()), float((err / (tol + 1e-38)).max())
     return out
@@ -403,6 +410,27 @@ def test_route_backward_ranges_of_values():
     dlg = torch.randn(T, E, device="cuda", generator=gen(28)) * \
         10 ** (torch.rand(1, E, device="cuda", generator=gen(29)) * 15 - 12)
     check_route_backward(layer, x, W, None, None, None, dlg.contiguous(), "softmax")
+    layer.close()
+
+
+def test_route_backward_sizes_of_router_weights():
+    # weights down to where f16 steps are absolute, and up to the limit
+    T, H, E = 130, 256, 32
+    x = acts(T, H, 42)
+    dlg = torch.randn(T, E, device="cuda", generator=gen(43))
+    for scale in (1e-6, 1e-3, 30.0):
+        W = router(E, H, 44) * scale
+        layer = make_layer(E, 2, H=H, W=W)
+        check_route_backward(layer, x, W, None, None, None, dlg, "softmax")
+        layer.close()
+    W = router(E, H, 44)
+    W[3, 7] = 256.0
+    layer = make_layer(E, 2, H=H, W=W)
+    run_route_backward(layer, x, None, None, None, dlg)
+    st, bits = layer.status()
+    assert st == binding.Status.RANGE and bits == 16
+    out = run_route_backward(layer, x, None, None, None, dlg, ("dW", "db"))   # W is not read
+    assert int(layer.status()[0]) == 0 and not bool(out["dW"].isnan().any())
     layer.close()
 
 
@@ -514,11 +542,13 @@ def test_gradients_against_differences(mode):
         step[e, c] = d
         num = (value(W.double() + step, x.double()) - value(W.double() - step, x.double())) / (2 * d)
         assert abs(num - float(out["dW"][e, c])) < 2e-5
+    dl, _ = exact_dl(logits, idx, dw, dlg, mode)
+    room = dx_rounding(dl, W)
     for t, c in ((0, 5), (11, 100)):
         step = torch.zeros(T, H, dtype=torch.float64, device="cuda")
         step[t, c] = d
         num = (value(W.double(), x.double() + step) - value(W.double(), x.double() - step)) / (2 * d)
-        assert abs(num - float(out["dx"][t, c])) < 2e-5 + abs(num) * 2.0 ** -8
+        assert abs(num - float(out["dx"][t, c])) < 2e-5 + abs(num) * 2.0 ** -8 + float(room[t, c])
     layer.close()
 
 
