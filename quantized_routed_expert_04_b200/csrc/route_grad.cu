@@ -58,40 +58,73 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// The gradient of token t's selected logits through its routing weights: lane
-// j < k gets selection j's expert (-1: none) and gradient.
-__device__ __forceinline__ void weight_grad(const RouteGradParams &p, int t, int lane, int &id,
-                                            float &g) {
-  const bool sel = lane < p.k;
-  id = sel ? p.idx[(size_t)t * p.k + lane] : -1;
-  const float dw = sel ? p.dw[(size_t)t * p.k + lane] : 0.0f;
-  const bool bad = sel && (id < 0 || id >= p.E);
-  // (a token with a bad id: the forward writes it a zero row, dw has no meaning)
+// A token's inputs: lane j < k its selection j, every lane 8 logits' gradients.
+struct TokenIn {
+  int id;
+  float dw, l;
+  float dl[8];
+};
+// Everything but the selected logit (whose place the id gives).
+__device__ __forceinline__ void load_token(const RouteGradParams &p, long long t, int lane, bool vec,
+                                           TokenIn &in) {
+  in.id = -1;
+  in.dw = in.l = 0.0f;
+  if (p.dw && t < p.T && lane < p.k) {
+    in.id = p.idx[t * p.k + lane];
+    in.dw = p.dw[t * p.k + lane];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) in.dl[i] = 0.0f;
+  if (!p.dlogits || t >= p.T) return;
+  const float *row = p.dlogits + t * p.E + 8 * lane;
+  if (vec) {
+    if (8 * lane < p.E) {
+      const float4 a = reinterpret_cast<const float4 *>(row)[0];
+      const float4 b = reinterpret_cast<const float4 *>(row)[1];
+      in.dl[0] = a.x; in.dl[1] = a.y; in.dl[2] = a.z; in.dl[3] = a.w;
+      in.dl[4] = b.x; in.dl[5] = b.y; in.dl[6] = b.z; in.dl[7] = b.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (8 * lane + i < p.E) in.dl[i] = row[i];
+  }
+}
+// The selected logits; a token with an id out of range (the forward writes it a
+// zero row, so dw has no meaning) loses its selections.
+__device__ __forceinline__ void load_selected(const RouteGradParams &p, long long t, int lane, TokenIn &in) {
+  if (!p.dw) return;
+  const bool sel = t < p.T && lane < p.k;
+  const bool bad = sel && (in.id < 0 || in.id >= p.E);
   const bool any_bad = __any_sync(0xffffffffu, bad);
   if (bad) set_status(p.status, STATUS_BAD_ROUTING);
-  const bool use = sel && !any_bad;
-  const float l = use ? p.logits[(size_t)t * p.E + id] : 0.0f;
+  if (any_bad) in.id = -1;
+  if (sel && in.id >= 0) in.l = p.logits[t * p.E + in.id];
+}
+
+// Lane j: the gradient of selection j's logit through the routing weights.
+__device__ __forceinline__ float weight_grad(const RouteGradParams &p, const TokenIn &in) {
+  const bool use = in.id >= 0;
   float w, slope;   // w_j / scale, and its factor in the gradient
   if (p.mode.sigmoid) {
-    const float ex = expf(-l);
+    const float ex = expf(-in.l);
     const float s = use ? __fdiv_rn(1.0f, 1.0f + ex) : 0.0f;
     const float z = warp_sum(s);
     // (a true division: one selected expert has w = 1 and no gradient)
     w = z == 0.0f ? 0.0f : __fdiv_rn(s, z);
     slope = s == 0.0f ? 0.0f : p.mode.scale * w * (ex * s);
   } else {
-    float m = use ? l : __int_as_float(0xff800000);
+    float m = use ? in.l : __int_as_float(0xff800000);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const bool none = m == __int_as_float(0xff800000);
-    const float ex = !use || (none && l == m) ? 0.0f : expf(l - m);
+    const float ex = !use || (none && in.l == m) ? 0.0f : expf(in.l - m);
     const float z = warp_sum(ex);
     w = z == 0.0f ? 0.0f : __fdiv_rn(ex, z);
     slope = w;
   }
-  const float dot = warp_sum(use ? w * dw : 0.0f);
-  g = use ? slope * (dw - dot) : 0.0f;
-  id = use ? id : -1;
+  const float dot = warp_sum(use ? w * in.dw : 0.0f);
+  return use ? slope * (in.dw - dot) : 0.0f;
 }
 
 // Eight floats -> f16.
@@ -130,31 +163,13 @@ __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const 
   float db[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) db[i] = 0.0f;
-  for (int t = blockIdx.x * kPrepWarps + warp; t < p.T; t += p.tok_blocks * kPrepWarps) {
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    if (p.dlogits) {
-      const float *row = p.dlogits + (size_t)t * E + 8 * lane;
-      if (vec) {
-        if (8 * lane < E) {
-          const float4 a = reinterpret_cast<const float4 *>(row)[0];
-          const float4 b = reinterpret_cast<const float4 *>(row)[1];
-          v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-          v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (8 * lane + i < E) v[i] = row[i];
-      }
-    }
+  auto finish = [&](long long t, TokenIn &in) {
+    if (t >= p.T) return;
+    float (&v)[8] = in.dl;
     if (p.dw) {
-      int id;
-      float g;
-      weight_grad(p, t, lane, id, g);
+      const float g = weight_grad(p, in);
       for (int j = 0; j < p.k; ++j) {
-        const int at = __shfl_sync(0xffffffffu, id, j) - 8 * lane;
+        const int at = __shfl_sync(0xffffffffu, in.id, j) - 8 * lane;
         const float gj = __shfl_sync(0xffffffffu, g, j);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += at == i ? gj : 0.0f;
@@ -181,6 +196,17 @@ __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const 
       out[plane] = take_bf16(v);
       out[2 * plane] = take_bf16(v);
     }
+  };
+  // two tokens a turn: their loads are in flight together
+  const long long step = (long long)p.tok_blocks * kPrepWarps;
+  for (long long t = (long long)blockIdx.x * kPrepWarps + warp; t < p.T; t += 2 * step) {
+    TokenIn a, b;
+    load_token(p, t, lane, vec, a);
+    load_token(p, t + step, lane, vec, b);
+    load_selected(p, t, lane, a);
+    load_selected(p, t + step, lane, b);
+    finish(t, a);
+    finish(t + step, b);
   }
   if (p.db_part) {
 #pragma unroll
@@ -533,33 +559,44 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 struct SumParams {
   RouteGradParams g;
   int pairs;          // runs of the dW kernel
-  int dw_quads;       // groups of four h to add up: tiles * E * 64, or 0
+  int dw_rows;        // rows of 256 h to add up: tiles * E, or 0
 };
 
-// Four consecutive h of one expert and tile.
-__device__ __forceinline__ void sum_dw(const SumParams &q, int i) {
+// One warp: expert e's 256 h of one tile, 8 a lane.
+__device__ __forceinline__ void sum_dw(const SumParams &q, int tile, int e, int lane) {
   const RouteGradParams &p = q.g;
   const int tiles = (p.H + kTileH - 1) / kTileH, n_kb = (p.T + kDwTok - 1) / kDwTok;
-  const int h4 = i % (kTileH / 4) * 4, te = i / (kTileH / 4);
-  const int tile = te / p.E, e = te - tile * p.E;
-  if (tile * kTileH + h4 >= p.H) return;
   // the runs that hold units of this tile (run r starts at unit units r / pairs)
   const long long units = (long long)tiles * n_kb, first = (long long)tile * n_kb;
   const int r0 = (int)(((first + 1) * q.pairs - 1) / units);
   const int r1 = (int)(((first + n_kb) * q.pairs - 1) / units);
   if (r0 == r1) return;   // one run had the whole tile and wrote it
-  const float *part = p.dW_part + ((size_t)(r0 + tile) * p.E + e) * kTileH + h4;
-  float4 s = __ldcg(reinterpret_cast<const float4 *>(part));
-#pragma unroll 4
-  for (int r = r0 + 1; r <= r1; ++r) {
-    part += (size_t)p.E * kTileH;
-    const float4 v = __ldcg(reinterpret_cast<const float4 *>(part));
-    s.x += v.x;
-    s.y += v.y;
-    s.z += v.z;
-    s.w += v.w;
+  const float4 *part =
+      reinterpret_cast<const float4 *>(p.dW_part + ((size_t)(r0 + tile) * p.E + e) * kTileH) + lane;
+  const size_t step = (size_t)p.E * kTileH / 4;
+  float4 s[2] = {};
+  for (int r = r0; r <= r1; r += 4) {
+    float4 v[4][2];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        v[k][c] = r + k <= r1 ? __ldcg(part + k * step + 32 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    part += 4 * step;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        s[c].x += v[k][c].x;
+        s[c].y += v[k][c].y;
+        s[c].z += v[k][c].z;
+        s[c].w += v[k][c].w;
+      }
   }
-  *reinterpret_cast<float4 *>(p.dW + (size_t)e * p.H + tile * kTileH + h4) = s;
+  float4 *out = reinterpret_cast<float4 *>(p.dW + (size_t)e * p.H + tile * kTileH) + lane;
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    if (tile * kTileH + 128 * c < p.H) out[32 * c] = s[c];
 }
 // One warp: expert e.
 __device__ __forceinline__ void sum_db(const RouteGradParams &p, int e, int lane) {
@@ -574,8 +611,10 @@ __device__ __forceinline__ void sum_db(const RouteGradParams &p, int e, int lane
 __device__ __forceinline__ void sum_parts(const SumParams &q, int warp, int warps, int lane) {
   if (q.g.db)
     for (int e = warp; e < q.g.E; e += warps) sum_db(q.g, e, lane);
-#pragma unroll 2
-  for (int i = warp * 32 + lane; i < q.dw_quads; i += warps * 32) sum_dw(q, i);
+  for (int i = warp; i < q.dw_rows; i += warps) {
+    const int tile = i / q.g.E;
+    sum_dw(q, tile, i - tile * q.g.E, lane);
+  }
 }
 // ... in a launch of its own, where dx is not wanted.
 __global__ void __launch_bounds__(256) route_grad_sum_kernel(const SumParams q) {
@@ -767,16 +806,10 @@ int prep_blocks(int T) {
   return n < 4 * kPairs ? n : 4 * kPairs;
 }
 int h_tiles(int H) { return (H + kTileH - 1) / kTileH; }
-// Pairs of blocks for dW: all of them, unless that leaves a run fewer than four
-// stages; then one per tile or a whole number per tile (every part of a tile
-// costs a write and a read of 256 rows).
+// Pairs of blocks for dW: all of them, as long as each gets a stage.
 int dw_pairs(int T, int H) {
-  const int tiles = h_tiles(H), n_kb = (T + kDwTok - 1) / kDwTok;
-  const long long units = (long long)tiles * n_kb;
-  if (units >= 4 * kPairs) return kPairs;
-  const int per = n_kb / 4 > 1 ? n_kb / 4 : 1;
-  const int n = tiles * per;
-  return n < kPairs ? n : kPairs;
+  const long long units = (long long)h_tiles(H) * ((T + kDwTok - 1) / kDwTok);
+  return units < kPairs ? (int)units : kPairs;
 }
 
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -855,7 +888,7 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
     if (e == cudaSuccess)
       e = launch_pdl_cluster(kern, dim3(2 * pairs), 2, dim3(kTcThreads), smem, stream, d, mx, md);
   }
-  const SumParams q{p, pairs, p.dW && tiles % pairs != 0 ? tiles * p.E * (kTileH / 4) : 0};
+  const SumParams q{p, pairs, p.dW && tiles % pairs != 0 ? tiles * p.E : 0};
   if (e == cudaSuccess && p.dx) {
     CUtensorMap md, mw, mo;
     if (!encode_planes(&md, kF16, p.dl16, p.E, p.T, p.Epad, 1, kDxTok / 2) ||
@@ -867,12 +900,14 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
                p.status};
     const int smem = fixed + d.stages * kDxStage + 1024;
     const long long items = (long long)((p.T + kDxTok - 1) / kDxTok) * tiles;
+    // (pairs without an item of dx help with the sums: a row of 256 per warp)
+    const long long want = std::max<long long>(items, (q.dw_rows + 2 * kSumWarps - 1) / (2 * kSumWarps));
     e = cudaFuncSetAttribute(route_grad_dx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
-      e = launch_pdl_cluster(route_grad_dx_kernel, dim3(2 * (unsigned)std::min<long long>(items, kPairs)),
+      e = launch_pdl_cluster(route_grad_dx_kernel, dim3(2 * (unsigned)std::min<long long>(want, kPairs)),
                              2, dim3(kDxThreads), smem, stream, d, q, md, mw, mo);
-  } else if (e == cudaSuccess && (p.db || q.dw_quads)) {
-    const int blocks = std::max((p.E + 7) / 8, (q.dw_quads + 255) / 256);
+  } else if (e == cudaSuccess && (p.db || q.dw_rows)) {
+    const int blocks = (std::max(p.E, q.dw_rows) + 7) / 8;
     e = launch_pdl(route_grad_sum_kernel, dim3(blocks), dim3(256), 0, stream, q);
   }
   return e;
