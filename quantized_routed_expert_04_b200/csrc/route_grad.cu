@@ -140,7 +140,10 @@ constexpr float kWScale = 256.0f;
 // lane 8 consecutive experts, as three bf16 pieces and as scaled f16, and the
 // block's share of db.  The blocks behind them: W as f16.
 __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const RouteGradParams p) {
-  __shared__ float s_db[kPrepWarps][kMaxExperts];
+  // a row per warp: the scattered selections, at the end the sums for db
+  __shared__ __align__(16) float s_row[kPrepWarps][kMaxExperts];
+  for (int i = threadIdx.x; i < kPrepWarps * kMaxExperts; i += blockDim.x) (&s_row[0][0])[i] = 0.0f;
+  __syncthreads();
   grid_dependency_wait();
   grid_dependency_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = p.E;
@@ -167,13 +170,28 @@ __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const 
     if (t >= p.T) return;
     float (&v)[8] = in.dl;
     if (p.dw) {
-      const float g = weight_grad(p, in);
-      for (int j = 0; j < p.k; ++j) {
-        const int at = __shfl_sync(0xffffffffu, in.id, j) - 8 * lane;
-        const float gj = __shfl_sync(0xffffffffu, g, j);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += at == i ? gj : 0.0f;
+      // scattered through a row of shared memory that is zero in between; of
+      // lanes with the same expert the first adds up all, in lane order
+      float g = weight_grad(p, in);
+      const unsigned same = __match_any_sync(0xffffffffu, in.id);
+      const bool first = (same & ((1u << lane) - 1u)) == 0u && in.id >= 0;
+      if (__any_sync(0xffffffffu, in.id >= 0 && (same & (same - 1u)) != 0u)) {
+        float sum = 0.0f;
+        for (int j = 0; j < p.k; ++j) {
+          const float gj = __shfl_sync(0xffffffffu, g, j);
+          if ((same >> j) & 1u) sum += gj;
+        }
+        g = sum;
       }
+      float *row = s_row[warp];
+      if (first) row[in.id] = g;
+      __syncwarp();
+      const float4 a = reinterpret_cast<const float4 *>(row)[2 * lane];
+      const float4 b = reinterpret_cast<const float4 *>(row)[2 * lane + 1];
+      v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+      v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+      __syncwarp();
+      if (first) row[in.id] = 0.0f;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) db[i] += v[i];
@@ -210,12 +228,12 @@ __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const 
   }
   if (p.db_part) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_db[warp][8 * lane + i] = db[i];
+    for (int i = 0; i < 8; ++i) s_row[warp][8 * lane + i] = db[i];
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
-      float s = s_db[0][e];
+      float s = s_row[0][e];
 #pragma unroll
-      for (int w = 1; w < kPrepWarps; ++w) s += s_db[w][e];
+      for (int w = 1; w < kPrepWarps; ++w) s += s_row[w][e];
       p.db_part[(size_t)blockIdx.x * E + e] = s;
     }
   }
@@ -410,12 +428,26 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int la
 //
 // The tensor core cuts its running sum at every MMA (2^-23 relative, always
 // towards zero): over one chain of 910 tokens, 168 MMAs, dW came out 2.7e-6 too
-// small.  So a chain is kDwChain stages (48 MMAs); the epilogue warps add the
+// small.  So a chain is 48 MMAs long; the epilogue warps add the
 // chains in fp32 registers, rounding to nearest, while the other accumulator
 // takes the next chain.
+//
+// An MMA costs about 115 cycles at N = 128 and 128 at N = 256, so the pieces of
+// dl share MMAs where the experts leave room (the pair's first block loads the
+// first half of the columns, the second the rest):
+//   form 0, up to 64 experts:   one MMA: hi 64 | mid 64 | lo 64 | (not used)
+//   form 1, up to 128 experts:  two: hi 128 | mid 128, then lo 128 on top of hi
+//   form 2, up to 256 experts:  three: hi, mid, lo, 256 columns each
+// and the epilogue adds the columns of an expert.
 constexpr int kDwTok = 32;
 constexpr int kDwBox = kDwTok * 128;   // 64 columns
-constexpr int kDwChain = 8;
+template <int kForm>
+struct DwForm {
+  static constexpr int kCols = 32 << kForm;                  // experts per epilogue warp
+  static constexpr int kSums = 3 - kForm;                    // column groups to add per expert
+  static constexpr int kBoxes = kForm == 0 ? 2 : 3 * kForm;  // of dl, per block and stage
+  static constexpr int kChain = kForm == 0 ? 24 : kForm == 1 ? 12 : 8;   // stages: 48 MMAs on hi
+};
 
 struct DwParams {
   int T, H, E, pairs, stages;
@@ -427,8 +459,7 @@ __host__ __device__ inline long long run_begin(long long units, int pairs, int i
   return units * i / pairs;
 }
 
-// kBoxes: boxes of 64 experts per block (N = 128 kBoxes)
-template <int kBoxes>
+template <int kForm>
 __global__ void __launch_bounds__(kTcThreads, 1)
     route_grad_dw_kernel(const DwParams p, const __grid_constant__ CUtensorMap map_x,
                          const __grid_constant__ CUtensorMap map_dl) {
@@ -446,7 +477,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   grid_dependency_wait();
   grid_dependency_launch();
 
-  constexpr int kStage = (2 + 3 * kBoxes) * kDwBox;   // per block
+  using F = DwForm<kForm>;
+  constexpr int kStage = (2 + F::kBoxes) * kDwBox;   // per block
   const int n_kb = (p.T + kDwTok - 1) / kDwTok;
   const int tiles = (p.H + kTileH - 1) / kTileH;
   const int pair = blockIdx.x >> 1;
@@ -462,15 +494,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int tile = (int)(u / n_kb), t = (int)(u - (long long)tile * n_kb) * kDwTok;
         uint8_t *a = smem + r.st * kStage, *b = a + 2 * kDwBox;
         const uint32_t bar = cluster_addr(&s.full[r.st], 0);
-        if (rank == 0) mbar_arrive_expect_tx(&s.full[r.st], 2 * kStage);
+        if (rank == 0) mbar_arrive_expect_tx(&s.full[r.st], 2 * kStage - (kForm == 0 ? kDwBox : 0));
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           tma2_load_2d(a + i * kDwBox, &map_x, tile * kTileH + 128 * (int)rank + 64 * i, t, bar);
+        const int rk = (int)rank;
+        auto piece = [&](int box, int c, int e) {
+          tma2_load_3d(b + box * kDwBox, &map_dl, e, t, c, bar);
+        };
+        if (kForm == 0) {
+          piece(0, 2 * rk, 0);
+          if (rk == 0) piece(1, 1, 0);
+        } else if (kForm == 1) {
+          piece(0, rk, 0);
+          piece(1, rk, 64);
+          piece(2, 2, 64 * rk);
+        } else {
 #pragma unroll
-        for (int c = 0; c < 3; ++c)
-#pragma unroll
-          for (int i = 0; i < kBoxes; ++i)
-            tma2_load_3d(b + (c * kBoxes + i) * kDwBox, &map_dl, 64 * (kBoxes * (int)rank + i), t, c, bar);
+          for (int c = 0; c < 3; ++c) {
+            piece(2 * c, c, 128 * rk);
+            piece(2 * c + 1, c, 128 * rk + 64);
+          }
+        }
         ++issued;
         r.next(p.stages);
       }
@@ -481,12 +526,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   } else if (warp == 1) {
     if (rank == 0) {
       Ring r;
-      const uint32_t idesc = umma_idesc_16(true, 256, 128 * kBoxes, true, true);
+      const uint32_t idesc = umma_idesc_16(true, 256, 256, true, true);
+      const uint32_t idesc_lo = umma_idesc_16(true, 256, 128, true, true);   // form 1
       int n = 0;   // chains
       bool ok = true;
       for (long long u = u0; u < u1 && ok; ++n) {
         const int tile = (int)(u / n_kb);
-        const long long end = min(min(u1, (long long)(tile + 1) * n_kb), u + kDwChain);
+        const long long end = min(min(u1, (long long)(tile + 1) * n_kb), u + F::kChain);
         const int buf = n & 1;
         if (!warp_wait(&s.acc_empty[buf], ((n >> 1) & 1u) ^ 1u, lane, p.status)) break;
         tc_fence_after();
@@ -499,12 +545,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const uint64_t ad = umma_desc_mn_sw128(a, kDwBox);
           const uint64_t bd = umma_desc_mn_sw128(a + 2 * kDwBox, kDwBox);
 #pragma unroll
-          for (int c = 0; c < 3; ++c)
-#pragma unroll
-            for (int ks = 0; ks < kDwTok / 16; ++ks) {
-              umma2_f16(d, ad + ks * (2048 >> 4), bd + c * (kBoxes * kDwBox >> 4) + ks * (2048 >> 4), idesc, more);
-              more = 1u;
+          for (int ks = 0; ks < kDwTok / 16; ++ks) {
+            const uint64_t ak = ad + ks * (2048 >> 4), bk = bd + ks * (2048 >> 4);
+            umma2_f16(d, ak, bk, idesc, ks > 0 ? 1u : more);
+            if (kForm == 1) umma2_f16(d, ak, bk + (2 * kDwBox >> 4), idesc_lo, 1u);
+            if (kForm == 2) {
+              umma2_f16(d, ak, bk + (2 * kDwBox >> 4), idesc, 1u);
+              umma2_f16(d, ak, bk + (4 * kDwBox >> 4), idesc, 1u);
             }
+          }
+          more = 1u;
           umma2_commit(&s.empty[r.st]);
           r.next(p.stages);
         }
@@ -513,8 +563,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else {
     // lane: one h; column: one expert.  Each warp holds a quarter of the lanes
-    // and half of the columns.
-    constexpr int kCols = 64 * kBoxes;
+    // and half of the experts.
+    constexpr int kCols = F::kCols;
     const int qd = warp & 3, half = (warp - 2) >> 2;
     const int hh = 128 * (int)rank + 32 * qd + lane;
     const uint32_t empty_bar[2] = {cluster_addr(&s.acc_empty[0], 0), cluster_addr(&s.acc_empty[1], 0)};
@@ -527,17 +577,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       float acc[kCols];
 #pragma unroll
       for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
-      for (; u < end; u += kDwChain, ++n) {
+      for (; u < end; u += F::kChain, ++n) {
         const int buf = n & 1;
         if (!warp_wait(&s.acc_full[buf], (n >> 1) & 1u, lane, p.status)) { ok = false; break; }
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < kCols; c += 16) {
-          float v[16];
-          tmem_ld_32x32b_x16(tmem + ((uint32_t)(32 * qd) << 16) + buf * 256 + half * kCols + c, v);
+        for (int g = 0; g < F::kSums; ++g)   // (the small pieces' columns last)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[c + i] += v[i];
-        }
+          for (int c = 0; c < kCols; c += 16) {
+            float v[16];
+            tmem_ld_32x32b_x16(tmem + ((uint32_t)(32 * qd) << 16) + buf * 256 + 2 * kCols * g +
+                                   half * kCols + c, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[c + i] += v[i];
+          }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) cluster_arrive(empty_bar[buf]);
@@ -879,11 +932,15 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
     if (!encode_planes(&mx, kBf16, p.x, p.H, p.T, p.H, 1, kDwTok) ||
         !encode_planes(&md, kBf16, p.dlp, p.E, p.T, p.Epad, 3, kDwTok))
       return cudaErrorInvalidValue;
-    const int boxes = p.E > 128 ? 2 : 1, stage = (2 + 3 * boxes) * kDwBox;
+    const int form = p.E <= 64 ? 0 : p.E <= 128 ? 1 : 2;
+    const int stage = (2 + (form == 0 ? DwForm<0>::kBoxes : form == 1 ? DwForm<1>::kBoxes
+                                                                      : DwForm<2>::kBoxes)) * kDwBox;
     DwParams d{p.T, p.H, p.E, pairs, std::min(kMaxStages, (kSmemLimit - 2048) / stage), p.dW, p.dW_part,
                p.status};
     const int smem = d.stages * stage + 1024;
-    auto kern = boxes == 2 ? route_grad_dw_kernel<2> : route_grad_dw_kernel<1>;
+    auto kern = form == 0   ? route_grad_dw_kernel<0>
+                : form == 1 ? route_grad_dw_kernel<1>
+                            : route_grad_dw_kernel<2>;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
       e = launch_pdl_cluster(kern, dim3(2 * pairs), 2, dim3(kTcThreads), smem, stream, d, mx, md);
