@@ -377,7 +377,7 @@ struct PairShared {
   uint32_t tmem;
 };
 
-__device__ __forceinline__ void pair_begin(PairShared &s, int stages, int warp) {
+__device__ __forceinline__ void pair_begin(PairShared &s, int stages, int epi_warps, int warp) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) {
       mbar_init(&s.full[i], 1);
@@ -385,7 +385,7 @@ __device__ __forceinline__ void pair_begin(PairShared &s, int stages, int warp) 
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.acc_full[i], 1);
-      mbar_init(&s.acc_empty[i], 2 * kEpiWarps);
+      mbar_init(&s.acc_empty[i], 2 * epi_warps);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&s.w_full[i], 1);
     mbar_init(&s.w_empty, 1);
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     prefetch_tmap(&map_x);
     prefetch_tmap(&map_dl);
   }
-  pair_begin(s, p.stages, warp);
+  pair_begin(s, p.stages, kEpiWarps, warp);
   const uint32_t tmem = s.tmem, rank = cluster_rank();
   grid_dependency_wait();
   grid_dependency_launch();
@@ -687,8 +687,9 @@ constexpr int kDxTok = 256;
 constexpr int kDxStage = kDxTok / 2 * 128;   // per block
 constexpr int kDxWBox = 64 * 128;
 constexpr int kDxOut = 32 * 128;             // 32 tokens x 64 h of bf16
+constexpr int kDxEpiWarps = 16;
 constexpr int kSumWarps = 4;
-constexpr int kDxThreads = kTcThreads + 32 * kSumWarps;
+constexpr int kDxThreads = 32 * (2 + kDxEpiWarps + kSumWarps);
 
 struct DxParams {
   int T, H, E, stages;
@@ -710,7 +711,7 @@ __global__ void __launch_bounds__(kDxThreads, 1)
     prefetch_tmap(&map_w);
     prefetch_tmap(&map_dx);
   }
-  pair_begin(s, p.stages, warp);
+  pair_begin(s, p.stages, kDxEpiWarps, warp);
   const uint32_t tmem = s.tmem, rank = cluster_rank();
   grid_dependency_wait();
   grid_dependency_launch();
@@ -722,7 +723,7 @@ __global__ void __launch_bounds__(kDxThreads, 1)
   const long long i0 = run_begin(items, pairs, pair), i1 = run_begin(items, pairs, pair + 1);
   uint8_t *w_smem = smem;                              // [k block][half of the block's 128 h]
   uint8_t *ring = smem + n_kb * 2 * kDxWBox;
-  uint8_t *out_smem = ring + p.stages * kDxStage;      // [epilogue warp][2]
+  uint8_t *out_smem = ring + p.stages * kDxStage;      // [epilogue warp]
   if (warp == 0) {
     if (lane == 0) {
       Ring r;
@@ -798,12 +799,12 @@ __global__ void __launch_bounds__(kDxThreads, 1)
         if (i + 1 < i1 && (int)((i + 1) / t_tiles) != cur) umma2_commit(&s.w_empty);
       }
     }
-  } else if (warp < 2 + kEpiWarps) {
+  } else if (warp < 2 + kDxEpiWarps) {
     // lane: one token; column: one h.  Each warp: a quarter of the block's 128
-    // tokens and half of the columns, 64 at a time.
-    const int qd = warp & 3, half = (warp - 2) >> 2;
+    // tokens and 64 of the columns.
+    const int qd = warp & 3, col = 64 * ((warp - 2) >> 2);
     const uint32_t empty_bar[2] = {cluster_addr(&s.acc_empty[0], 0), cluster_addr(&s.acc_empty[1], 0)};
-    uint8_t *tile = out_smem + (warp - 2) * 2 * kDxOut;
+    uint8_t *tile = out_smem + (warp - 2) * kDxOut;
     int n = 0;
     for (long long i = i0; i < i1; ++i, ++n) {
       const int h = (int)(i / t_tiles), t0 = (int)(i - (long long)h * t_tiles) * kDxTok;
@@ -812,41 +813,36 @@ __global__ void __launch_bounds__(kDxThreads, 1)
       const int buf = n & 1;
       if (!warp_wait(&s.acc_full[buf], (n >> 1) & 1u, lane, p.status)) break;
       tc_fence_after();
+      // the tile's last store has read it
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      __syncwarp();
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int col = 128 * half + 64 * b;
-        uint32_t o[32];
-#pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          float v[32];
-          tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * qd) << 16) + buf * 256 + col + c, v);
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            o[c / 2 + k] = bf162_bits(__floats2bfloat162_rn(v[2 * k] * scale, v[2 * k + 1] * scale));
-        }
-        if (b == 1) {   // the accumulator is in registers
+      for (int c = 0; c < 2; ++c) {
+        float v[32];
+        tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * qd) << 16) + buf * 256 + col + 32 * c, v);
+        if (c == 1) {   // the accumulator is in registers
           tc_fence_before();
           __syncwarp();
           if (lane == 0) cluster_arrive(empty_bar[buf]);
         }
-        // the tile's last store has read it
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        __syncwarp();
-        uint8_t *dst = tile + b * kDxOut + lane * 128;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          *reinterpret_cast<uint4 *>(dst + ((k ^ (lane & 7)) << 4)) =
-              make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-        fence_async_smem();
-        __syncwarp();
-        const int h0 = h * kTileH + col;   // H is a multiple of 128
-        if (lane == 0 && h0 < p.H && tok0 < p.T) tma_store_2d(&map_dx, tile + b * kDxOut, h0, tok0);
-        __syncwarp();
+        for (int k = 0; k < 4; ++k) {
+          uint32_t o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            o[j] = bf162_bits(__floats2bfloat162_rn(v[8 * k + 2 * j] * scale, v[8 * k + 2 * j + 1] * scale));
+          *reinterpret_cast<uint4 *>(tile + lane * 128 + (((4 * c + k) ^ (lane & 7)) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+        }
       }
+      fence_async_smem();
+      __syncwarp();
+      const int h0 = h * kTileH + col;   // H is a multiple of 128
+      if (lane == 0 && h0 < p.H && tok0 < p.T) tma_store_2d(&map_dx, tile, h0, tok0);
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   } else {
-    sum_parts(q, blockIdx.x * kSumWarps + warp - 2 - kEpiWarps, gridDim.x * kSumWarps, lane);
+    sum_parts(q, blockIdx.x * kSumWarps + warp - 2 - kDxEpiWarps, gridDim.x * kSumWarps, lane);
   }
   pair_end(s, warp);
 }
@@ -952,7 +948,7 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
         !encode_planes(&mw, kF16, p.W16, p.H, p.E, p.H, 1, 64) ||
         !encode_planes(&mo, kBf16, p.dx, p.H, p.T, p.H, 1, 32))
       return cudaErrorInvalidValue;
-    const int fixed = (p.E + 63) / 64 * 2 * kDxWBox + kEpiWarps * 2 * kDxOut;
+    const int fixed = (p.E + 63) / 64 * 2 * kDxWBox + kDxEpiWarps * kDxOut;
     DxParams d{p.T, p.H, p.E, std::min(kMaxStages, (kSmemLimit - 2048 - fixed) / kDxStage), p.t_scale,
                p.status};
     const int smem = fixed + d.stages * kDxStage + 1024;
