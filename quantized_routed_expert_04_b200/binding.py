@@ -280,11 +280,10 @@ def _rows(t, shape, dtype, dev, where):
 
 
 def _flat(t, dev, n, itemsize, where):
-    """Address of a contiguous operand of n elements of itemsize bytes, or None."""
+    """Address of a contiguous operand of n * itemsize bytes, or None."""
     if t is None:
         return None
-    if (t.numel() != n or t.element_size() != itemsize or t.get_device() != dev
-            or not t.is_contiguous()):
+    if t.nbytes != n * itemsize or t.get_device() != dev or not t.is_contiguous():
         _refuse(where)
     return t.data_ptr()
 
@@ -295,7 +294,7 @@ def _workspace(t, dev, where):
         return None, 0
     if t.get_device() != dev or not t.is_contiguous():
         _refuse(where)
-    return t.data_ptr(), t.numel() * t.element_size()
+    return t.data_ptr(), t.nbytes
 
 
 def _on_current(dev, where):

@@ -61,9 +61,10 @@ __device__ __forceinline__ int first_seq(const BalanceParams &p, int t) {
   return lo;
 }
 
-// Experts 8 j .. 8 j + 7 of a row (-inf past the last).
+// Experts 8 j .. 8 j + 7 of a row (-inf past the last, or all of them if !use),
+// in pairs: the arithmetic below runs two to an instruction.
 template <bool kVec>
-__device__ __forceinline__ void load_row8(const float *row, int j, int E, bool use, float v[8]) {
+__device__ __forceinline__ void load_row8(const float *row, int j, int E, bool use, float2 v[4]) {
   const float none = __int_as_float(0xff800000);
   if (kVec) {
     float4 a = make_float4(none, none, none, none), b = a;
@@ -71,11 +72,16 @@ __device__ __forceinline__ void load_row8(const float *row, int j, int E, bool u
       a = __ldg(reinterpret_cast<const float4 *>(row + 8 * j));
       b = __ldg(reinterpret_cast<const float4 *>(row + 8 * j + 4));
     }
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    v[0] = make_float2(a.x, a.y);
+    v[1] = make_float2(a.z, a.w);
+    v[2] = make_float2(b.x, b.y);
+    v[3] = make_float2(b.z, b.w);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = use && 8 * j + i < E ? __ldg(row + 8 * j + i) : none;
+    for (int i = 0; i < 4; ++i) {
+      v[i].x = use && 8 * j + 2 * i < E ? __ldg(row + 8 * j + 2 * i) : none;
+      v[i].y = use && 8 * j + 2 * i + 1 < E ? __ldg(row + 8 * j + 2 * i + 1) : none;
+    }
   }
 }
 
@@ -104,49 +110,73 @@ __device__ __forceinline__ float lanes_max(float v) {
   return v;
 }
 
-// v: logits of the lane's experts -> p.  slope (if wanted): the factor of
-// u (f_e - sum f p) in the gradient.  A row without any probability (every
-// logit -inf, or every sigmoid zero) gives zeros.
+__device__ __forceinline__ float2 pair(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float min_nan(float a, float b) {   // a NaN stays one
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(b));
+  return a;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(b));
+  return a;
+}
+__device__ __forceinline__ float exp2_approx(float v) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v));
+  return e;
+}
+__device__ __forceinline__ float rcp_approx(float v) {   // within 1 unit; 0 from 2^126 on
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+// e^-y for y in [-88, 110], as 2^(t - r): t = -y log2 e rounded, r what the
+// rounding left out (the product's error by an FMA, plus y times the low part of
+// log2 e), 2^-r = 1 - r ln 2.  The instruction's own error of 2^-22 is all that
+// remains; below 2^-126 the result is 0.
+__device__ __forceinline__ float2 exp_minus(float2 y) {
+  constexpr double kLog2e = 1.4426950408889634074;
+  constexpr float kHi = (float)kLog2e, kLo = (float)(kLog2e - (double)kHi);
+  const float2 t = __fmul2_rn(y, pair(-kHi));
+  float2 r = __ffma2_rn(y, pair(kHi), t);
+  r = __ffma2_rn(y, pair(kLo), r);
+  const float2 e = make_float2(exp2_approx(t.x), exp2_approx(t.y));
+  return __ffma2_rn(e, __fmul2_rn(r, pair(-0.69314718f)), e);
+}
+
+// v: logits of the lane's experts -> terms proportional to p; returns the
+// factor that makes them p (0 for a row without any probability: every logit
+// -inf, or every sigmoid zero).  slope (if wanted): the same multiple of the
+// factor of u (f_e - sum f p) in the gradient.
 template <int kLanes, bool kSlope>
-__device__ __forceinline__ void probabilities(float v[8], bool sigmoid, float slope[8]) {
+__device__ __forceinline__ float probabilities(float2 v[4], bool sigmoid, float2 slope[4]) {
+  float2 z = make_float2(0.0f, 0.0f);
   if (!sigmoid) {
-    float m = v[0];
+    float m = fmaxf(v[0].x, v[0].y);
 #pragma unroll
-    for (int i = 1; i < 8; ++i) m = fmaxf(m, v[i]);
+    for (int i = 1; i < 4; ++i) m = fmaxf(m, fmaxf(v[i].x, v[i].y));
     m = lanes_max<kLanes>(m);
-    const bool none = m == __int_as_float(0xff800000);
-    float z = 0.0f;
+    if (m == __int_as_float(0xff800000)) m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = none && v[i] == m ? 0.0f : expf(v[i] - m);
-      z += v[i];
-    }
-    z = lanes_sum<kLanes>(z);
-    const float r = z == 0.0f ? 0.0f : __fdiv_rn(1.0f, z);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] *= r;
+    for (int i = 0; i < 4; ++i) {
+      const float2 y = __ffma2_rn(v[i], pair(-1.0f), pair(m));   // >= 0
+      v[i] = exp_minus(make_float2(min_nan(y.x, 110.0f), min_nan(y.y, 110.0f)));
+      z = __fadd2_rn(z, v[i]);
       if (kSlope) slope[i] = v[i];
     }
   } else {
-    float z = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float ex = expf(-v[i]);
-      const float s = __fdividef(1.0f, 1.0f + ex);   // within 1 unit, 0 beyond 2^126
-      // s (1 - s) with 1 - s = ex s, or 1 where ex is beyond fp32 (s = 0)
-      if (kSlope) slope[i] = s == 0.0f ? 0.0f : s * (ex * s);
-      v[i] = s;
-      z += s;
-    }
-    z = lanes_sum<kLanes>(z);
-    const float r = z == 0.0f ? 0.0f : __fdiv_rn(1.0f, z);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] *= r;
-      if (kSlope) slope[i] *= r;
+    for (int i = 0; i < 4; ++i) {
+      // ex = e^-l; s = 1 / (1 + ex) (0 from 2^126 on) and 1 - s = ex s
+      const float2 ex = exp_minus(make_float2(max_nan(min_nan(v[i].x, 110.0f), -88.0f),
+                                              max_nan(min_nan(v[i].y, 110.0f), -88.0f)));
+      const float2 d = __fadd2_rn(ex, pair(1.0f));
+      v[i] = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+      if (kSlope) slope[i] = __fmul2_rn(v[i], __fmul2_rn(ex, v[i]));
+      z = __fadd2_rn(z, v[i]);
     }
   }
+  const float total = lanes_sum<kLanes>(z.x + z.y);
+  return total == 0.0f ? 0.0f : rcp_approx(total);
 }
 
 // The block's share of one sequence's tokens [a, e): sums of p per expert into
@@ -162,44 +192,56 @@ __device__ __forceinline__ void sum_piece(const BalanceParams &p, int a, int e, 
   for (int i = tid; i < E; i += kSumThreads) s_cnt[i] = 0;
   if (tid == 0) *s_tok = 0;
   __syncthreads();
-  float acc[8];
+  float2 acc[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+  for (int i = 0; i < 4; ++i) acc[i] = pair(0.0f);
   int n = 0;
-  auto counted = [&](int tok) { return tok < e && (!p.mask || p.mask[tok] != 0); };
-  // the next token's row is loaded before this one's is reduced
-  float next[8];
-  bool next_live = counted(a + warp * kTok + sub);
-  load_row8<kVec>(p.logits + (size_t)(a + warp * kTok + sub) * E, j, E, next_live, next);
-  for (int t0 = a + warp * kTok; t0 < e; t0 += kWarps * kTok) {
-    const int tok = t0 + sub;
+  // Three tokens are in flight: this one's terms, the next one's row and first
+  // id, and the mask of the one after (so that no load waits for another).
+  constexpr int kStep = kWarps * kTok;
+  auto mask_of = [&](int tok) { return tok < e && (!p.mask || p.mask[tok] != 0); };
+  auto first_id = [&](int tok, bool use) {
+    return use && j < k ? p.idx[(size_t)tok * k + j] : -1;
+  };
+  auto count = [&](int id) {   // integers: any order
+    if (id < 0 || id >= E)
+      set_status(p.status, STATUS_BAD_ROUTING);
+    else
+      atomicAdd(&s_cnt[id], 1);
+  };
+  float2 next[4];
+  int tok = a + warp * kTok + sub;
+  bool next_live = mask_of(tok), later = mask_of(tok + kStep);
+  load_row8<kVec>(p.logits + (size_t)tok * E, j, E, next_live, next);
+  int next_id = first_id(tok, next_live);
+  for (int t0 = a + warp * kTok; t0 < e; t0 += kStep, tok += kStep) {
     const bool live = next_live;
-    float v[8];
+    const int id = next_id;
+    float2 v[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = next[i];
-    const int ahead = tok + kWarps * kTok;
-    next_live = counted(ahead);
-    load_row8<kVec>(p.logits + (size_t)ahead * E, j, E, next_live, next);
-    if (live) {   // counts: integers, in any order
-      for (int i = j; i < k; i += kLanes) {
-        const int id = p.idx[(size_t)tok * k + i];
-        if (id < 0 || id >= E)
-          set_status(p.status, STATUS_BAD_ROUTING);
-        else
-          atomicAdd(&s_cnt[id], 1);
-      }
+    for (int i = 0; i < 4; ++i) v[i] = next[i];
+    next_live = later;
+    load_row8<kVec>(p.logits + (size_t)(tok + kStep) * E, j, E, next_live, next);
+    next_id = first_id(tok + kStep, next_live);
+    later = mask_of(tok + 2 * kStep);
+    if (live && j < k) {
+      count(id);
+      for (int i = j + kLanes; i < k; i += kLanes) count(p.idx[(size_t)tok * k + i]);
     }
     __syncwarp();
-    probabilities<kLanes, false>(v, p.sigmoid, nullptr);
+    // (a token that does not count was not loaded: its terms are finite)
+    float r = probabilities<kLanes, false>(v, p.sigmoid, nullptr);
+    r = live ? r : 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] += live ? v[i] : 0.0f;
+    for (int i = 0; i < 4; ++i) acc[i] = __ffma2_rn(v[i], pair(r), acc[i]);
     n += live && j == 0;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
+    float a1 = i % 2 ? acc[i / 2].y : acc[i / 2].x;
 #pragma unroll
-    for (int o = kLanes; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-    if (sub == 0) s_p[warp][8 * j + i] = acc[i];
+    for (int o = kLanes; o < 32; o <<= 1) a1 += __shfl_xor_sync(0xffffffffu, a1, o);
+    if (sub == 0) s_p[warp][8 * j + i] = a1;
   }
   n = __reduce_add_sync(0xffffffffu, n);
   if (lane == 0 && n) atomicAdd(s_tok, n);
@@ -233,13 +275,13 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceP
       double all = 0.0;
       for (int i = tid; i < E; i += 32) {
         p.counts[i] = s_cnt[i];
-        if (nb > 0) all += (double)s_cnt[i] * E / ((double)p.k * nb) * ((double)s_p[0][i] / nb);
+        all += (double)s_cnt[i] * (double)s_p[0][i];
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
       if (tid == 0) {
         p.tokens[0] = nb;
-        p.loss[0] = (float)((double)p.coef * all);
+        p.loss[0] = nb > 0 ? (float)((double)p.coef * all * E / ((double)p.k * nb * nb)) : 0.0f;
       }
     }
     return;
@@ -264,8 +306,8 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceP
 }
 
 // A cluster of blocks per sequence, 32 experts a block: adds the slots of the
-// sequence's pieces, writes its counts; the first block adds up the sum of
-// f P over the cluster.
+// sequence's pieces, writes its counts; the first block adds up the sum
+// of counts x (sum of p) over the cluster, which is f P up to E / (k n^2).
 __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(const BalanceParams p) {
   __shared__ double s_p[32][33];
   __shared__ int s_c[32][33];
@@ -310,7 +352,7 @@ __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(const Ba
   __syncthreads();
   if (lane == 0) {
     if (xe < E) p.counts[(size_t)b * E + xe] = cnt;
-    s_p[0][y] = xe < E && nb > 0 ? (double)cnt * E / ((double)p.k * nb) * (sum / nb) : 0.0;
+    s_p[0][y] = xe < E ? (double)cnt * sum : 0.0;
   }
   __syncthreads();
   if (y == 0) {
@@ -320,14 +362,18 @@ __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(const Ba
     if (lane == 0) s_term = term;
   }
   cluster_sync();
-  if (blockIdx.x == 0 && tid == 0) {
-    double all = 0.0;
-    for (int r = 0; r < (int)gridDim.x; ++r) all += cluster_read(&s_term, r);
-    p.tokens[b] = nb;
-    if (p.n_seq == 1)
-      p.loss[0] = (float)((double)p.coef * all);
-    else
-      p.seq_loss[b] = all;
+  if (blockIdx.x == 0 && y == 0) {
+    double all = lane < (int)gridDim.x ? cluster_read(&s_term, lane) : 0.0;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);   // <= 8 blocks
+    if (lane == 0) {
+      p.tokens[b] = nb;
+      all = nb > 0 ? all * E / ((double)p.k * nb * nb) : 0.0;
+      if (p.n_seq == 1)
+        p.loss[0] = (float)((double)p.coef * all);
+      else
+        p.seq_loss[b] = all;
+    }
   }
   cluster_sync();   // no block leaves while its s_term may still be read
 }
@@ -361,48 +407,52 @@ __global__ void __launch_bounds__(kGradThreads) balance_grad_kernel(const Balanc
   const int t_end = min(p.T, t + p.chunk);
   const float dloss = g.dloss ? *g.dloss : 1.0f;
   // tokens [a, e) with the weights f and the factor u (zeros if !counted)
-  auto piece = [&](int a, int e, bool counted, const float f[8], float u) {
+  auto piece = [&](int a, int e, bool counted, const float2 f[4], float u) {
     // last token first: the forward's last rows are still in L2, where the
-    // batch as a whole does not fit; the next row is loaded ahead
+    // batch as a whole does not fit.  The next row and the mask after it are
+    // loaded ahead
     constexpr int kStep = kGradThreads / 32 * kTok;
-    auto used = [&](int tok) {
+    auto mask_of = [&](int tok) {
       return counted && tok >= a && (!p.mask || p.mask[tok] != 0);
     };
     int tok = e - 1 - warp * kTok - sub;
-    float next[8];
-    bool next_live = used(tok);
+    float2 next[4];
+    bool next_live = mask_of(tok), later = mask_of(tok - kStep);
     load_row8<kVec>(p.logits + (long long)tok * E, j, E, next_live, next);
     for (int t1 = e - 1 - warp * kTok; t1 >= a; t1 -= kStep, tok -= kStep) {
       const bool in = tok >= a;
       const bool live = next_live;
-      float v[8], slope[8];
+      float2 v[4], slope[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = next[i];
-      next_live = used(tok - kStep);
+      for (int i = 0; i < 4; ++i) v[i] = next[i];
+      next_live = later;
+      later = mask_of(tok - 2 * kStep);
       load_row8<kVec>(p.logits + ((long long)tok - kStep) * E, j, E, next_live, next);
-      probabilities<kLanes, true>(v, p.sigmoid, slope);
-      float dot = 0.0f;
+      const float r = probabilities<kLanes, true>(v, p.sigmoid, slope);
+      float2 d2 = pair(0.0f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dot = fmaf(f[i], v[i], dot);
-      dot = lanes_sum<kLanes>(dot);
+      for (int i = 0; i < 4; ++i) d2 = __ffma2_rn(f[i], v[i], d2);
+      const float dot = lanes_sum<kLanes>(d2.x + d2.y) * r;
+      const float ur = live ? u * r : 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = live ? u * slope[i] * (f[i] - dot) : 0.0f;
+      for (int i = 0; i < 4; ++i)
+        v[i] = __fmul2_rn(__fmul2_rn(slope[i], pair(ur)), __fadd2_rn(f[i], pair(-dot)));
       float *out = g.dlogits + (long long)tok * E + 8 * j;
       if (kVec) {
         if (in && 8 * j < E) {
-          reinterpret_cast<float4 *>(out)[0] = make_float4(v[0], v[1], v[2], v[3]);
-          reinterpret_cast<float4 *>(out)[1] = make_float4(v[4], v[5], v[6], v[7]);
+          reinterpret_cast<float4 *>(out)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+          reinterpret_cast<float4 *>(out)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (in && 8 * j + i < E) out[i] = v[i];
+          if (in && 8 * j + i < E) out[i] = i % 2 ? v[i / 2].y : v[i / 2].x;
       }
     }
   };
-  float f[8];
+  float2 f[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = 0.0f;
+  for (int i = 0; i < 4; ++i) f[i] = pair(0.0f);
   for (int b = first_seq(p, t); b < p.n_seq && t < t_end; ++b) {
     const Span sp = seq_span(p, b);
     const int a = max(sp.a, t), e = min(sp.e, t_end);
@@ -411,10 +461,13 @@ __global__ void __launch_bounds__(kGradThreads) balance_grad_kernel(const Balanc
     const int nb = p.tokens[b];
     const float inv = nb > 0 ? __fdiv_rn(1.0f, (float)nb) : 0.0f;
     const float per = (float)E / (float)p.k * inv;
-    float fb[8];
+    float2 fb[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      fb[i] = 8 * j + i < E ? (float)p.counts[(size_t)b * E + 8 * j + i] * per : 0.0f;
+    for (int i = 0; i < 8; ++i) {
+      const float one = 8 * j + i < E ? (float)p.counts[(size_t)b * E + 8 * j + i] * per : 0.0f;
+      if (i % 2) fb[i / 2].y = one;
+      else fb[i / 2].x = one;
+    }
     piece(a, e, true, fb, dloss * (p.coef / (float)p.n_seq) * inv);
     t = e;
   }
