@@ -460,7 +460,7 @@ strata_status strata_moe_forward_q8(strata_moe *h, const void *x_q8, const float
  * workspace: device memory, 16-byte aligned, of at least the size that the
  * *_workspace call gives for the same arguments, written before it is read.
  * Calls that may overlap on the GPU, and graphs that may be replayed at once,
- * need a workspace each.  At most 2^28 tokens and sequences a call.
+ * need a workspace each.  At most 2^28 tokens and 2^17 sequences a call.
  *
  * Balance loss of a batch's routing, and how many tokens each expert got.
  * logits: device fp32 [n_tokens][n_experts]; idx: device int32

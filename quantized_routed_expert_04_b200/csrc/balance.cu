@@ -31,7 +31,7 @@ namespace {
 constexpr int kSumThreads = 1024;    // forward: one block per multiprocessor
 constexpr int kGradThreads = 256;
 constexpr int kFinishThreads = 1024;
-constexpr int kMaxGridY = 65535;
+constexpr int kFinishSeqs = 4;       // sequences of a cluster of the finishing kernel
 
 __device__ __forceinline__ int clamp_int(int v, int lo, int hi) { return min(max(v, lo), hi); }
 
@@ -305,74 +305,111 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceP
   }
 }
 
-// A cluster of blocks per sequence, 32 experts a block: adds the slots of the
-// sequence's pieces, writes its counts; the first block adds up the sum
-// of counts x (sum of p) over the cluster, which is f P up to E / (k n^2).
+// Adds the slots of each sequence's pieces.  A cluster takes up to 4 sequences
+// (kOne: the only one), each of its blocks 32 experts; of a block's 32 warps, as
+// many as there are sequences for share one sequence's slots.  The kernel is
+// nothing but latency (packed batch of 37 sequences, whole pass: 84.8 us with 4
+// sequences a cluster, 85.5 with 16, 92.7 with 64, which saves the last launch
+// but takes two turns).  Writes the counts, and
+// adds sum over experts of counts x (sum of p), which is f P up to
+// E / (k n^2), over the cluster: its first block writes the loss (one cluster)
+// or each sequence's sum.
+template <bool kOne>
 __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(const BalanceParams p) {
-  __shared__ double s_p[32][33];
-  __shared__ int s_c[32][33];
-  __shared__ int s_tok;
-  __shared__ double s_term;
+  constexpr int kWarps = kFinishThreads / 32;
+  __shared__ double s_p[kWarps][32];
+  __shared__ int s_c[kWarps][32], s_t[kWarps];
+  __shared__ double s_term[kFinishSeqs];
+  __shared__ int s_tok[kFinishSeqs];
   grid_dependency_wait();
   grid_dependency_launch();
-  const int b = p.seq0 + blockIdx.y, tid = threadIdx.x, E = p.E;
-  const Span sp = seq_span(p, b);
-  if (p.seq_off && tid == 0 && (p.seq_off[b] != sp.a || p.seq_off[b + 1] != sp.e))
-    set_status(p.status, STATUS_BOUNDS);
-  const int c0 = sp.a / p.chunk;
-  const int n = sp.e > sp.a ? (sp.e - 1) / p.chunk - c0 + 1 : 0;
-  if (tid == 0) s_tok = 0;
-  __syncthreads();
-  const int lane = tid & 31, y = tid >> 5;   // expert of the block, share of the slots
-  const int x = blockIdx.x * 32 + lane;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = p.E;
+  const int b0 = kOne ? 0 : blockIdx.y * kFinishSeqs;
+  const int nb = kOne ? 1 : min(kFinishSeqs, p.n_seq - b0);
+  const int x = blockIdx.x * 32 + lane;              // the lane's expert
+  // warp: share warp % shares of sequence q
+  const int shares = kOne ? kWarps : kWarps / nb;
+  const int q = kOne ? 0 : warp / shares, share = kOne ? warp : warp % shares;
+  const bool mine = q < nb;
   double sum = 0.0;
   int cnt = 0, tok = 0;
-  for (int i = tid; i < n; i += kFinishThreads) tok += p.part_tok[c0 + i + b];
-  if (x < E) {
-#pragma unroll 5
-    for (int i = y; i < n; i += 32) {
-      const size_t slot = (size_t)c0 + i + b;
-      sum += (double)p.part_p[slot * E + x];
-      cnt += p.part_cnt[slot * E + x];
+  if (mine) {
+    const int b = b0 + q;
+    const Span sp = seq_span(p, b);
+    if (p.seq_off && share == 0 && lane == 0 && (p.seq_off[b] != sp.a || p.seq_off[b + 1] != sp.e))
+      set_status(p.status, STATUS_BOUNDS);
+    const int c0 = sp.a / p.chunk;
+    const int n = sp.e > sp.a ? (sp.e - 1) / p.chunk - c0 + 1 : 0;
+    // (at most 148 slots: five loads a lane; they are waited for at the end)
+    int t[5];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+      const int i = share + (lane + 32 * k) * shares;
+      t[k] = i < n ? p.part_tok[c0 + i + b] : 0;
     }
+    // several slots at a time, each load under its own condition (a loop's
+    // remainder would take them one by one)
+    constexpr int kAtOnce = kOne ? 5 : 8;
+    for (int i0 = share; i0 < n; i0 += kAtOnce * shares) {
+      float v[kAtOnce];
+      int c[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int i = i0 + k * shares;
+        const size_t at = ((size_t)c0 + i + b) * E + x;
+        const bool in = i < n && x < E;
+        v[k] = in ? p.part_p[at] : 0.0f;
+        c[k] = in ? p.part_cnt[at] : 0;
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        sum += (double)v[k];
+        cnt += c[k];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 5; ++k) tok += t[k];
   }
   tok = __reduce_add_sync(0xffffffffu, tok);
-  if (lane == 0 && tok) atomicAdd(&s_tok, tok);
-  s_p[y][lane] = sum;
-  s_c[y][lane] = cnt;
+  s_p[warp][lane] = sum;
+  s_c[warp][lane] = cnt;
+  if (lane == 0) s_t[warp] = tok;
   __syncthreads();
-  const int nb = s_tok;
-  // warp y: the 32 shares of expert 32 blockIdx.x + y
-  sum = s_p[lane][y];
-  cnt = s_c[lane][y];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  cnt = __reduce_add_sync(0xffffffffu, cnt);
-  const int xe = blockIdx.x * 32 + y;
-  __syncthreads();
-  if (lane == 0) {
-    if (xe < E) p.counts[(size_t)b * E + xe] = cnt;
-    s_p[0][y] = xe < E ? (double)cnt * sum : 0.0;
-  }
-  __syncthreads();
-  if (y == 0) {
-    double term = s_p[0][lane];
+  if (mine && share == 0) {
+#pragma unroll 8
+    for (int w = 1; w < kWarps; ++w) {
+      if (w >= shares) break;
+      sum += s_p[warp + w][lane];
+      cnt += s_c[warp + w][lane];
+      tok += s_t[warp + w];
+    }
+    if (x < E) p.counts[(size_t)(b0 + q) * E + x] = cnt;
+    double term = (double)cnt * sum;   // 0 for lanes without an expert
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
-    if (lane == 0) s_term = term;
-  }
-  cluster_sync();
-  if (blockIdx.x == 0 && y == 0) {
-    double all = lane < (int)gridDim.x ? cluster_read(&s_term, lane) : 0.0;
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);   // <= 8 blocks
     if (lane == 0) {
-      p.tokens[b] = nb;
-      all = nb > 0 ? all * E / ((double)p.k * nb * nb) : 0.0;
-      if (p.n_seq == 1)
-        p.loss[0] = (float)((double)p.coef * all);
-      else
-        p.seq_loss[b] = all;
+      s_term[q] = term;
+      s_tok[q] = tok;
+    }
+  }
+  __syncthreads();
+  cluster_sync();
+  if (blockIdx.x == 0) {
+    for (int q = threadIdx.x; q < nb; q += kFinishThreads) {
+      double all = 0.0;
+      for (int r = 0; r < (int)gridDim.x; ++r) all += cluster_read(&s_term[q], r);
+      const int n = s_tok[q];
+      p.tokens[b0 + q] = n;
+      all = n > 0 ? all * E / ((double)p.k * n * n) : 0.0;
+      s_p[0][q] = all;
+      if (gridDim.y > 1) p.seq_loss[b0 + q] = all;
+    }
+    __syncthreads();
+    if (gridDim.y == 1 && warp == 0) {
+      double all = lane < nb ? s_p[0][lane] : 0.0;
+#pragma unroll
+      for (int o = kFinishSeqs / 2; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+      if (lane == 0) p.loss[0] = (float)(all * (double)p.coef / p.n_seq);
     }
   }
   cluster_sync();   // no block leaves while its s_term may still be read
@@ -477,7 +514,7 @@ __global__ void __launch_bounds__(kGradThreads) balance_grad_kernel(const Balanc
 // Forward: tokens per block, a multiple of 32, that give each of the 148
 // multiprocessors one block of 32 warps.
 int sum_chunk(int T) { return std::max(32, ((T + 147) / 148 + 31) & ~31); }
-int sum_blocks(int T) { return (T + sum_chunk(T) - 1) / sum_chunk(T); }
+int sum_blocks(int T) { return (T + sum_chunk(T) - 1) / sum_chunk(T); }   // <= 148
 // Backward: up to four blocks of 8 warps each, at least two rows a warp.
 int grad_chunk(int T) {
   const int per = (T + 591) / 592;
@@ -548,13 +585,10 @@ cudaError_t run_balance(BalanceParams p, void *workspace, cudaStream_t stream) {
   cudaError_t e =
       by_shape<LaunchSum>(p.E, vec_rows(p.logits, p.E), (const BalanceParams *)&p, whole, stream);
   if (whole || e != cudaSuccess) return e;
-  for (int b0 = 0; e == cudaSuccess && b0 < p.n_seq; b0 += kMaxGridY) {
-    p.seq0 = b0;
-    const int groups = (p.E + 31) / 32;
-    e = launch_pdl_cluster(balance_finish_kernel, dim3(groups, std::min(p.n_seq - b0, kMaxGridY)),
-                           groups, dim3(kFinishThreads), 0, stream, p);
-  }
-  if (e == cudaSuccess && p.n_seq > 1)
+  const int groups = (p.E + 31) / 32, clusters = (p.n_seq + kFinishSeqs - 1) / kFinishSeqs;
+  e = launch_pdl_cluster(p.n_seq == 1 ? balance_finish_kernel<true> : balance_finish_kernel<false>,
+                         dim3(groups, clusters), groups, dim3(kFinishThreads), 0, stream, p);
+  if (e == cudaSuccess && clusters > 1)
     e = launch_pdl(balance_mean_kernel, dim3(1), dim3(256), 0, stream, p);
   return e;
 }

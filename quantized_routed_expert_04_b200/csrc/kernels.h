@@ -128,7 +128,6 @@ struct BalanceParams {
   int *status;
   // set by run_balance / run_balance_grad
   int chunk;               // tokens per block
-  int seq0;                // first sequence of the launch
   float *part_p;           // [blocks + n_seq][E] sums of p per piece
   int *part_cnt, *part_tok;
   double *seq_loss;        // [n_seq]

@@ -511,11 +511,16 @@ __global__ void __launch_bounds__(1024) norm_grad_sum_kernel(const float *partia
   grid_dependency_launch();
   const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
-  float v = 0.0f;
-  if (c < H) {
-#pragma unroll 10
-    for (int r = y; r < n; r += 32) v += partial[(long long)r * H + c];
+  // all of the thread's (at most 10) loads at once, each under its own condition
+  float t[10];
+#pragma unroll
+  for (int k = 0; k < 10; ++k) {
+    const int r = y + 32 * k;
+    t[k] = r < n && c < H ? partial[(long long)r * H + c] : 0.0f;
   }
+  float v = t[0];
+#pragma unroll
+  for (int k = 1; k < 10; ++k) v += t[k];
   s[y][lane] = v;
   __syncthreads();
   v = s[lane][y];   // row share lane of column y

@@ -654,8 +654,14 @@ __device__ __forceinline__ void sum_dw(const SumParams &q, int tile, int e, int 
 // One warp: expert e.
 __device__ __forceinline__ void sum_db(const RouteGradParams &p, int e, int lane) {
   double s = 0.0;
-#pragma unroll 4
-  for (int b = lane; b < p.tok_blocks; b += 32) s += __ldcg(p.db_part + (size_t)b * p.E + e);
+  float v[10];   // at most 296 blocks
+#pragma unroll
+  for (int k = 0; k < 10; ++k) {
+    const int b = lane + 32 * k;
+    v[k] = b < p.tok_blocks ? __ldcg(p.db_part + (size_t)b * p.E + e) : 0.0f;
+  }
+#pragma unroll
+  for (int k = 0; k < 10; ++k) s += (double)v[k];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (lane == 0) p.db[e] = (float)s;
@@ -849,6 +855,7 @@ __global__ void __launch_bounds__(kDxThreads, 1)
 
 // ---------------------------------------------------------------- host
 constexpr int kPairs = 74;   // 148 multiprocessors
+static_assert(4 * kPairs <= 320, "sum_db reads up to 320 blocks' parts");
 
 int prep_blocks(int T) {
   const int n = (T + kPrepWarps - 1) / kPrepWarps;

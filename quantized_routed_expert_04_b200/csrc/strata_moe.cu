@@ -812,9 +812,9 @@ strata_status strata_moe_profile_read(strata_moe *h, int n_phases, int *launches
 
 namespace {
 
-// Tokens (and sequences) of one training call: token numbers and block offsets
-// stay well inside 32 bits.
-constexpr int kMaxTrainTokens = 1 << 28;
+// Tokens of one training call (token numbers and block offsets stay well inside
+// 32 bits), and sequences (four to a row of the balance loss's grid).
+constexpr int kMaxTrainTokens = 1 << 28, kMaxTrainSeqs = 1 << 17;
 
 inline bool misaligned(const void *p, size_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0;
@@ -829,7 +829,7 @@ strata_status check_device(const strata_moe *h) {
 
 strata_status check_balance(const strata_moe *h, const float *logits, int T, const int32_t *seq_off,
                             int n_seq, float coef, const int32_t *counts, const int32_t *tokens) {
-  if (!h || T < 0 || T > kMaxTrainTokens || n_seq < 1 || n_seq > kMaxTrainTokens ||
+  if (!h || T < 0 || T > kMaxTrainTokens || n_seq < 1 || n_seq > kMaxTrainSeqs ||
       (!seq_off && n_seq != 1))
     return STRATA_ERR_INVALID_ARG;
   if (!(coef >= -3.0e38f) || !(coef <= 3.0e38f)) return STRATA_ERR_INVALID_ARG;
@@ -845,7 +845,7 @@ strata_status check_balance(const strata_moe *h, const float *logits, int T, con
 extern "C" {
 
 size_t strata_moe_balance_workspace(const strata_moe *h, int n_tokens, int n_seq) {
-  if (!h || n_tokens < 0 || n_tokens > kMaxTrainTokens || n_seq < 1 || n_seq > kMaxTrainTokens)
+  if (!h || n_tokens < 0 || n_tokens > kMaxTrainTokens || n_seq < 1 || n_seq > kMaxTrainSeqs)
     return 0;
   return balance_workspace(n_tokens, h->E, n_seq);
 }
