@@ -61,17 +61,22 @@ __device__ __forceinline__ int first_seq(const BalanceParams &p, int t) {
   return lo;
 }
 
-// Experts 8 j .. 8 j + 7 of a row (-inf past the last, or all of them if !use),
-// in pairs: the arithmetic below runs two to an instruction.
-template <bool kVec>
+// Expert i < 8 of lane j of a row: eight consecutive ones, or (rows that 16-byte
+// loads cannot walk) every kLanes-th, so that neighbouring lanes load neighbours.
+template <int kLanes, bool kVec>
+__device__ __forceinline__ int expert_of(int j, int i) {
+  return kVec ? 8 * j + i : j + kLanes * i;
+}
+
+// The lane's experts of a row (-inf past the last, or all of them if !use), in
+// pairs: the arithmetic below runs two to an instruction.
+template <int kLanes, bool kVec>
 __device__ __forceinline__ void load_row8(const float *row, int j, int E, bool use, float2 v[4]) {
   const float none = __int_as_float(0xff800000);
   if (kVec) {
     float4 a = make_float4(none, none, none, none), b = a;
-    if (use && 8 * j < E) {
-      a = __ldg(reinterpret_cast<const float4 *>(row + 8 * j));
-      b = __ldg(reinterpret_cast<const float4 *>(row + 8 * j + 4));
-    }
+    if (use && 8 * j < E) a = __ldg(reinterpret_cast<const float4 *>(row + 8 * j));
+    if (use && 8 * j + 4 < E) b = __ldg(reinterpret_cast<const float4 *>(row + 8 * j + 4));
     v[0] = make_float2(a.x, a.y);
     v[1] = make_float2(a.z, a.w);
     v[2] = make_float2(b.x, b.y);
@@ -79,8 +84,9 @@ __device__ __forceinline__ void load_row8(const float *row, int j, int E, bool u
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[i].x = use && 8 * j + 2 * i < E ? __ldg(row + 8 * j + 2 * i) : none;
-      v[i].y = use && 8 * j + 2 * i + 1 < E ? __ldg(row + 8 * j + 2 * i + 1) : none;
+      const int e0 = expert_of<kLanes, kVec>(j, 2 * i), e1 = expert_of<kLanes, kVec>(j, 2 * i + 1);
+      v[i].x = use && e0 < E ? __ldg(row + e0) : none;
+      v[i].y = use && e1 < E ? __ldg(row + e1) : none;
     }
   }
 }
@@ -212,7 +218,7 @@ __device__ __forceinline__ void sum_piece(const BalanceParams &p, int a, int e, 
   float2 next[4];
   int tok = a + warp * kTok + sub;
   bool next_live = mask_of(tok), later = mask_of(tok + kStep);
-  load_row8<kVec>(p.logits + (size_t)tok * E, j, E, next_live, next);
+  load_row8<kLanes, kVec>(p.logits + (size_t)tok * E, j, E, next_live, next);
   int next_id = first_id(tok, next_live);
   for (int t0 = a + warp * kTok; t0 < e; t0 += kStep, tok += kStep) {
     const bool live = next_live;
@@ -221,7 +227,7 @@ __device__ __forceinline__ void sum_piece(const BalanceParams &p, int a, int e, 
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = next[i];
     next_live = later;
-    load_row8<kVec>(p.logits + (size_t)(tok + kStep) * E, j, E, next_live, next);
+    load_row8<kLanes, kVec>(p.logits + (size_t)(tok + kStep) * E, j, E, next_live, next);
     next_id = first_id(tok + kStep, next_live);
     later = mask_of(tok + 2 * kStep);
     if (live && j < k) {
@@ -241,7 +247,7 @@ __device__ __forceinline__ void sum_piece(const BalanceParams &p, int a, int e, 
     float a1 = i % 2 ? acc[i / 2].y : acc[i / 2].x;
 #pragma unroll
     for (int o = kLanes; o < 32; o <<= 1) a1 += __shfl_xor_sync(0xffffffffu, a1, o);
-    if (sub == 0) s_p[warp][8 * j + i] = a1;
+    if (sub == 0) s_p[warp][expert_of<kLanes, kVec>(j, i)] = a1;
   }
   n = __reduce_add_sync(0xffffffffu, n);
   if (lane == 0 && n) atomicAdd(s_tok, n);
@@ -455,7 +461,7 @@ __global__ void __launch_bounds__(kGradThreads) balance_grad_kernel(const Balanc
     int tok = e - 1 - warp * kTok - sub;
     float2 next[4];
     bool next_live = mask_of(tok), later = mask_of(tok - kStep);
-    load_row8<kVec>(p.logits + (long long)tok * E, j, E, next_live, next);
+    load_row8<kLanes, kVec>(p.logits + (long long)tok * E, j, E, next_live, next);
     for (int t1 = e - 1 - warp * kTok; t1 >= a; t1 -= kStep, tok -= kStep) {
       const bool in = tok >= a;
       const bool live = next_live;
@@ -464,7 +470,7 @@ __global__ void __launch_bounds__(kGradThreads) balance_grad_kernel(const Balanc
       for (int i = 0; i < 4; ++i) v[i] = next[i];
       next_live = later;
       later = mask_of(tok - 2 * kStep);
-      load_row8<kVec>(p.logits + ((long long)tok - kStep) * E, j, E, next_live, next);
+      load_row8<kLanes, kVec>(p.logits + ((long long)tok - kStep) * E, j, E, next_live, next);
       const float r = probabilities<kLanes, true>(v, p.sigmoid, slope);
       float2 d2 = pair(0.0f);
 #pragma unroll
@@ -474,16 +480,17 @@ __global__ void __launch_bounds__(kGradThreads) balance_grad_kernel(const Balanc
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         v[i] = __fmul2_rn(__fmul2_rn(slope[i], pair(ur)), __fadd2_rn(f[i], pair(-dot)));
-      float *out = g.dlogits + (long long)tok * E + 8 * j;
+      float *out = g.dlogits + (long long)tok * E;
       if (kVec) {
-        if (in && 8 * j < E) {
-          reinterpret_cast<float4 *>(out)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-          reinterpret_cast<float4 *>(out)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
-        }
+        float4 *o4 = reinterpret_cast<float4 *>(out + 8 * j);
+        if (in && 8 * j < E) o4[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+        if (in && 8 * j + 4 < E) o4[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (in && 8 * j + i < E) out[i] = i % 2 ? v[i / 2].y : v[i / 2].x;
+        for (int i = 0; i < 8; ++i) {
+          const int x = expert_of<kLanes, kVec>(j, i);
+          if (in && x < E) out[x] = i % 2 ? v[i / 2].y : v[i / 2].x;
+        }
       }
     }
   };
@@ -501,7 +508,8 @@ __global__ void __launch_bounds__(kGradThreads) balance_grad_kernel(const Balanc
     float2 fb[4];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float one = 8 * j + i < E ? (float)p.counts[(size_t)b * E + 8 * j + i] * per : 0.0f;
+      const int x = expert_of<kLanes, kVec>(j, i);
+      const float one = x < E ? (float)p.counts[(size_t)b * E + x] * per : 0.0f;
       if (i % 2) fb[i / 2].y = one;
       else fb[i / 2].x = one;
     }
@@ -563,7 +571,7 @@ struct LaunchGrad {
 };
 
 inline bool vec_rows(const void *p, int E) {
-  return E % 8 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+  return E % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
 }
 
 }  // namespace

@@ -312,34 +312,40 @@ __global__ void __launch_bounds__(kTpr *kRows) norm_kernel(const NormParams p) {
     }
   } else {
     // a warp's 32 lanes hold columns 32 m .. 32 m + 31 of m = i * kTpr / 32 +
-    // warp: the group's magnitude is the largest over its group / 32 such runs
-    float *amax32 = s_amax + (threadIdx.x / kTpr) * kNe * (kTpr / 32);
-    const int per = per_row ? 1 : p.group / 32;
+    // warp: the largest magnitude of each such run, then a step per group
+    float *run = s_amax + (threadIdx.x / kTpr) * kNe * (kTpr / 32);
+    auto meet = [] {
+      if (kTpr > 32)
+        __syncthreads();
+      else
+        __syncwarp();
+    };
+    const float row_mul = per_row ? __fdiv_rn(1.0f, e4m3_step(row_amax)) : 0.0f;
     if (!per_row) {
 #pragma unroll
       for (int i = 0; i < kNe; ++i) {
         float a = fabsf(v[i]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
-        if ((tid & 31) == 0) amax32[i * (kTpr / 32) + (tid >> 5)] = a;
+        if ((tid & 31) == 0) run[i * (kTpr / 32) + (tid >> 5)] = a;
       }
-      if (kTpr > 32)
-        __syncthreads();
-      else
-        __syncwarp();
+      meet();
+      // group g: its runs' largest, its step, and 1 / step back to the runs
+      const int per = p.group / 32, runs = (H + 31) / 32;
+      for (int g = tid; g < p.n_groups; g += kTpr) {
+        float amax = 0.0f;
+        for (int m = g * per; m < min(g * per + per, runs); ++m) amax = max_nan(amax, run[m]);
+        const float step = e4m3_step(amax), mul = __fdiv_rn(1.0f, step);
+        scales[g] = step;
+        for (int m = g * per; m < min(g * per + per, runs); ++m) run[m] = mul;
+      }
+      meet();
     }
 #pragma unroll
     for (int i = 0; i < kNe; ++i) {
       const int c = tid + i * kTpr;
-      if (c >= H) break;
-      float amax = row_amax;
-      if (!per_row) {
-        const int m0 = (c >> 5) / per * per;
-        for (int m = m0; m < m0 + per && m * 32 < H; ++m) amax = max_nan(amax, amax32[m]);
-      }
-      const float step = e4m3_step(amax);
-      q8[c] = __nv_cvt_float_to_fp8(v[i] * __fdiv_rn(1.0f, step), __NV_SATFINITE, __NV_E4M3);
-      if (!per_row && c % p.group == 0) scales[c / p.group] = step;
+      const float mul = per_row ? row_mul : run[i * (kTpr / 32) + (tid >> 5)];
+      if (c < H) q8[c] = __nv_cvt_float_to_fp8(v[i] * mul, __NV_SATFINITE, __NV_E4M3);
     }
   }
 }
@@ -369,21 +375,29 @@ struct NormGradParams {
   int stages;                    // rows in flight per block
 };
 
-// One block walks rows blockIdx.x, + gridDim.x, ...; a thread keeps its
-// columns' weights and weight-gradient sums in registers over all of them.
-// With kVec the rows come through a ring of shared-memory stages filled by bulk
-// copies, so that several rows of all three inputs are in flight while one is
-// reduced: on 8192 rows of 4096 bf16, plain loads with one row in registers
-// ahead took 98 us (waiting for loads), the ring takes GRAD_US us.  The barrier
-// of the row's reduction also frees its stage: every thread has its elements
-// in registers by then.
-template <typename T, int kTpr, int kNe, bool kVec, int kMinBlocks>
-__global__ void __launch_bounds__(kTpr, kMinBlocks) norm_grad_kernel(const NormGradParams p) {
+// kRows groups of kTpr threads, each with rows of its own: group g of block b
+// walks rows b kRows + g, + gridDim.x kRows, ...; a thread keeps its columns'
+// weights (kKeepW) and weight-gradient sums in registers over all of them.
+// With kVec the rows come through a ring of shared-memory stages per group,
+// filled by bulk copies, so that several rows of all three inputs are in flight
+// while one is reduced: on 8192 rows of 4096 bf16 with a direct gradient, plain
+// loads with one row ahead in registers took 98 us (waiting for loads; and 88
+// through the ring with elements converted one by one), now 49 us.  The barrier
+// of the row's reduction also frees its stage: every thread has its elements in
+// registers by then.  Without kVec (rows that 16-byte copies cannot walk) the
+// next row's elements are loaded into registers ahead.
+template <typename T, int kTpr, int kRows, int kNe, bool kVec, int kMinBlocks>
+__global__ void __launch_bounds__(kTpr *kRows, kMinBlocks) norm_grad_kernel(const NormGradParams p) {
   constexpr int kWarps = kTpr / 32;
-  extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float2 s_red[2][kWarps];
-  __shared__ uint64_t full[kMaxStages];
-  const int tid = threadIdx.x, H = p.H;
+  // 1024 threads have 64 registers each: they keep only the sums in them and read
+  // the row from its stage twice; !kVec's next row takes the weights' registers
+  constexpr bool kHold = !kVec || kTpr < 1024;
+  constexpr bool kKeepW = kVec && kHold;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float2 s_red[kRows][2][kWarps];
+  __shared__ uint64_t s_full[kRows][kMaxStages];
+  const int tid = threadIdx.x % kTpr, group = threadIdx.x / kTpr, H = p.H;
+  uint64_t *full = s_full[group];
   const uint32_t row_bytes = (uint32_t)H * sizeof(T);
   const bool direct = p.dsum != nullptr;
   if (kVec) {
@@ -395,7 +409,18 @@ __global__ void __launch_bounds__(kTpr, kMinBlocks) norm_grad_kernel(const NormG
   }
   grid_dependency_wait();
   grid_dependency_launch();
+  // all threads of a row
+  auto meet = [&] {
+    if (kWarps == 1)
+      __syncwarp();
+    else if (kRows == 1)
+      __syncthreads();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kTpr) : "memory");
+  };
+  const long long row0 = (long long)blockIdx.x * kRows + group, step = (long long)gridDim.x * kRows;
   const uint32_t stage_bytes = row_bytes * (direct ? 3 : 2);
+  uint8_t *ring = smem + (size_t)group * p.stages * stage_bytes;
   auto fetch = [&](long long row, int st) {
     if (row >= p.T) return;
     uint8_t *dst = ring + st * stage_bytes;
@@ -406,47 +431,99 @@ __global__ void __launch_bounds__(kTpr, kMinBlocks) norm_grad_kernel(const NormG
       bulk_g2s(dst + 2 * row_bytes, static_cast<const T *>(p.dsum) + row * p.ldds, row_bytes, &full[st]);
   };
   if (kVec && tid == 0)
-    for (int s = 0; s < p.stages; ++s) fetch(blockIdx.x + (long long)s * gridDim.x, s);
+    for (int s = 0; s < p.stages; ++s) fetch(row0 + s * step, s);
   auto col = [&](int i) { return kVec ? (tid + (i / 8) * kTpr) * 8 + i % 8 : tid + i * kTpr; };
-  float dg[kNe], w[kNe];
+  constexpr int kAhead = kVec ? 1 : kNe;
+  T ha[kAhead], da[kAhead];   // !kVec: the next row
+  auto load_row = [&](long long row) {
+    if (kVec || row >= p.T) return;
+    const T *h = static_cast<const T *>(p.h) + row * p.ldh;
+    const T *dy = static_cast<const T *>(p.dout) + row * p.lddo;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (col(i) < H) {
+        ha[i] = h[col(i)];
+        da[i] = dy[col(i)];
+      }
+  };
+  load_row(row0);
+  float dg[kNe], w[kKeepW ? kNe : 1];
 #pragma unroll
   for (int i = 0; i < kNe; ++i) {
     dg[i] = 0.0f;
-    w[i] = col(i) < H ? __ldg(p.weight + col(i)) : 0.0f;
+    if (kKeepW) w[i] = col(i) < H ? __ldg(p.weight + col(i)) : 0.0f;
   }
+  auto weight = [&](int i) {
+    return kKeepW ? w[kKeepW ? i : 0] : col(i) < H ? __ldg(p.weight + col(i)) : 0.0f;
+  };
+  auto weight8 = [&](int i, float w8[8]) {   // of columns col(i) ..
+    if (kKeepW || !kVec) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w8[j] = weight(i + j);
+    } else if (col(i) < H) {
+      const float4 x = __ldg(reinterpret_cast<const float4 *>(p.weight + col(i)));
+      const float4 y = __ldg(reinterpret_cast<const float4 *>(p.weight + col(i) + 4));
+      w8[0] = x.x; w8[1] = x.y; w8[2] = x.z; w8[3] = x.w;
+      w8[4] = y.x; w8[5] = y.y; w8[6] = y.z; w8[7] = y.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w8[j] = 0.0f;
+    }
+  };
   int flip = 0, st = 0;
   uint32_t phase = 0;
-  for (long long row = blockIdx.x; row < p.T; row += gridDim.x, flip ^= 1) {
-    float a[kNe], d[kNe];
-    Vec8<T> sc[kVec ? kNe / 8 : 1];
+  for (long long row = row0; row < p.T; row += step, flip ^= 1) {
+    float a[kHold ? kNe : 8], d[kHold ? kNe : 8];
+    Vec8<T> sc[kVec && kHold ? kNe / 8 : 1];
+    T sn[kAhead];
+    float sq = 0.0f, dot = 0.0f;
+    const T *sh = reinterpret_cast<const T *>(ring + st * stage_bytes);
+    auto unpack_at = [&](int i, float *a8, float *d8) {
+      if (col(i) < H) {
+        unpack8(load8(sh + col(i)), a8);
+        unpack8(load8(sh + H + col(i)), d8);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a8[j] = d8[j] = 0.0f;
+      }
+    };
     if (kVec) {
       if (!mbar_wait(&full[st], phase, nullptr)) break;
-      const T *sh = reinterpret_cast<const T *>(ring + st * stage_bytes);
 #pragma unroll
       for (int i = 0; i < kNe; i += 8) {
-        const bool in = col(i) < H;
-        if (in) {
-          unpack8(load8(sh + col(i)), a + i);
-          unpack8(load8(sh + H + col(i)), d + i);
-          if (direct) sc[i / 8] = load8(sh + 2 * H + col(i));
+        unpack_at(i, a + (kHold ? i : 0), d + (kHold ? i : 0));
+        if (kHold) {
+          if (direct && col(i) < H) sc[i / 8] = load8(sh + 2 * H + col(i));
         } else {
+          float w8[8];
+          weight8(i, w8);
 #pragma unroll
-          for (int j = i; j < i + 8; ++j) a[j] = d[j] = 0.0f;
+          for (int j = 0; j < 8; ++j) {
+            sq = fmaf(a[j], a[j], sq);
+            dot = fmaf(d[j] * w8[j], a[j], dot);
+          }
         }
       }
     } else {
-      const T *h = static_cast<const T *>(p.h) + row * p.ldh;
-      const T *dy = static_cast<const T *>(p.dout) + row * p.lddo;
 #pragma unroll
-      for (int i = 0; i < kNe; ++i) a[i] = col(i) < H ? to_f32(h[col(i)]) : 0.0f;
+      for (int i = 0; i < kAhead; ++i) {
+        a[kVec ? 0 : i] = col(i) < H ? to_f32(ha[i]) : 0.0f;
+        d[kVec ? 0 : i] = col(i) < H ? to_f32(da[i]) : 0.0f;
+      }
+      if (direct) {
+        const T *ds = static_cast<const T *>(p.dsum) + row * p.ldds;
 #pragma unroll
-      for (int i = 0; i < kNe; ++i) d[i] = col(i) < H ? to_f32(dy[col(i)]) : 0.0f;
+        for (int i = 0; i < kAhead; ++i)
+          if (col(i) < H) sn[i] = ds[col(i)];
+      }
+      load_row(row + step);
     }
-    float sq = 0.0f, dot = 0.0f;
+    if (kHold) {
 #pragma unroll
-    for (int i = 0; i < kNe; ++i) {
-      sq = fmaf(a[i], a[i], sq);
-      dot = fmaf(d[i] * w[i], a[i], dot);
+      for (int i = 0; i < (kHold ? kNe : 0); ++i) {
+        sq = fmaf(a[i], a[i], sq);
+        dot = fmaf(d[i] * weight(i), a[i], dot);
+      }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -454,17 +531,18 @@ __global__ void __launch_bounds__(kTpr, kMinBlocks) norm_grad_kernel(const NormG
       dot += __shfl_xor_sync(0xffffffffu, dot, o);
     }
     // (two slots in turn: a warp is at most one row ahead of the others)
-    if (kWarps > 1 && (tid & 31) == 0) s_red[flip][tid >> 5] = make_float2(sq, dot);
-    if (kWarps > 1 || kVec) __syncthreads();
-    if (kVec) {
-      if (tid == 0) fetch(row + (long long)p.stages * gridDim.x, st);
+    if (kWarps > 1 && (tid & 31) == 0) s_red[group][flip][tid >> 5] = make_float2(sq, dot);
+    if (kWarps > 1 || kVec) meet();
+    auto next_stage = [&] {
+      if (tid == 0) fetch(row + p.stages * step, st);
       if (++st == p.stages) {
         st = 0;
         phase ^= 1u;
       }
-    }
+    };
+    if (kVec && kHold) next_stage();
     if (kWarps > 1) {
-      const float2 v = s_red[flip][tid & (kWarps - 1)];
+      const float2 v = s_red[group][flip][tid & (kWarps - 1)];
       sq = v.x;
       dot = v.y;
 #pragma unroll
@@ -476,29 +554,50 @@ __global__ void __launch_bounds__(kTpr, kMinBlocks) norm_grad_kernel(const NormG
     const float inv = rsqrtf(fmaf(sq, p.inv_h, p.eps));
     const float back = dot * p.inv_h * inv * inv;   // i^2 mean(gy h)
     T *dx = static_cast<T *>(p.dx) + row * p.lddx;
-    const T *ds = static_cast<const T *>(p.dsum) + row * p.ldds;
 #pragma unroll
     for (int i = 0; i < kNe; i += 8) {
-      float o[8], s[8];
-      if (kVec && direct) unpack8(sc[i / 8], s);
+      float o[8], s[8], w8[8];
+      if (!kHold) unpack_at(i, a, d);
+      weight8(i, w8);
+      if (kVec && direct && col(i) < H) unpack8(kHold ? sc[kHold ? i / 8 : 0] : load8(sh + 2 * H + col(i)), s);
 #pragma unroll
       for (int j = i; j < i + 8; ++j) {
-        dg[j] = fmaf(d[j], a[j] * inv, dg[j]);
-        o[j - i] = inv * (d[j] * w[j] - a[j] * back);
+        const float aj = a[kHold ? j : j - i], dj = d[kHold ? j : j - i];
+        dg[j] = fmaf(dj, aj * inv, dg[j]);
+        o[j - i] = inv * (dj * w8[j - i] - aj * back);
         if (kVec) {
           if (direct) o[j - i] += s[j - i];
         } else if (col(j) < H) {
-          dx[col(j)] = from_f32<T>(direct ? o[j - i] + to_f32(ds[col(j)]) : o[j - i]);
+          dx[col(j)] = from_f32<T>(direct ? o[j - i] + to_f32(sn[kVec ? 0 : j]) : o[j - i]);
         }
       }
       if (kVec && col(i) < H) store8(dx + col(i), pack8<T>(o));
     }
+    if (kVec && !kHold) {
+      meet();
+      next_stage();
+    }
   }
-  if (p.partial) {
-    float *out = p.partial + (long long)blockIdx.x * H;
+  if (!p.partial) return;
+  float *out = p.partial + (long long)blockIdx.x * H;
+  if (kRows == 1) {
 #pragma unroll
     for (int i = 0; i < kNe; ++i)
       if (col(i) < H) out[col(i)] = dg[i];
+    return;
+  }
+  // the groups' sums, in order, through shared memory (every stage has been read)
+  float *rows = reinterpret_cast<float *>(smem);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kNe; ++i)
+    if (col(i) < H) rows[group * H + col(i)] = dg[i];
+  __syncthreads();
+  for (int c = threadIdx.x; c < H; c += kTpr * kRows) {
+    float v = rows[c];
+#pragma unroll
+    for (int g = 1; g < kRows; ++g) v += rows[g * H + c];
+    out[c] = v;
   }
 }
 
@@ -530,36 +629,45 @@ __global__ void __launch_bounds__(1024) norm_grad_sum_kernel(const float *partia
   if (lane == 0 && cy < H) out[cy] = v;
 }
 
+// Rows that a block takes at once: 256 threads have a row of at most 4096
+// elements, smaller ones share the block.
+inline int grad_rows(int H) { return H <= 512 ? 8 : H <= 1024 ? 4 : H <= 2048 ? 2 : 1; }
 // Blocks of the gradient kernel: two for each of the 148 multiprocessors, half
-// as many where that leaves a block fewer than four rows (each block's partial
-// sums are as long as a row and are read again).
-inline int grad_blocks(int T) { return T >= 1184 ? 296 : T < 148 ? T : 148; }
+// as many where that leaves a group of threads fewer than four rows (each
+// block's partial sums are as long as a row and are read again).
+inline int grad_blocks(int T, int H) {
+  const long long need = ((long long)T + grad_rows(H) - 1) / grad_rows(H);
+  return need >= 1184 ? 296 : need < 148 ? (int)need : 148;
+}
 
-template <typename T, int kTpr, int kNe, bool kVec, int kMinBlocks>
+template <typename T, int kTpr, int kRows, int kNe, bool kVec, int kMinBlocks>
 cudaError_t launch_norm_grad_as(NormGradParams p, cudaStream_t stream) {
-  auto kern = norm_grad_kernel<T, kTpr, kNe, kVec, kMinBlocks>;
-  int smem = 0;
+  auto kern = norm_grad_kernel<T, kTpr, kRows, kNe, kVec, kMinBlocks>;
+  int smem = kRows > 1 ? kRows * p.H * (int)sizeof(float) : 0;   // the groups' sums
+  p.stages = 0;
   if (kVec) {
     // two blocks share a multiprocessor's 227 KB, or one takes it (a row of
     // 16384 fp32 elements and its two gradients are 192 KB)
     const int stage = p.H * (int)sizeof(T) * (p.dsum ? 3 : 2);
-    p.stages = std::min(kMaxStages, std::max(1, (kMinBlocks > 1 ? 110 : 220) * 1024 / stage));
-    smem = p.stages * stage;
+    p.stages = std::min(kMaxStages, std::max(1, (kMinBlocks > 1 ? 110 : 220) * 1024 / (kRows * stage)));
+    smem = std::max(smem, kRows * p.stages * stage);
+  }
+  if (smem > 0) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(kern, dim3(grad_blocks(p.T)), dim3(kTpr), smem, stream, p);
+  return launch_pdl(kern, dim3(grad_blocks(p.T, p.H)), dim3(kTpr * kRows), smem, stream, p);
 }
 
 template <typename T, bool kVec>
 cudaError_t launch_norm_grad(const NormGradParams &p, cudaStream_t stream) {
-  if (p.H <= 256) return launch_norm_grad_as<T, 32, 8, kVec, 2>(p, stream);
-  if (p.H <= 512) return launch_norm_grad_as<T, 64, 8, kVec, 2>(p, stream);
-  if (p.H <= 1024) return launch_norm_grad_as<T, 64, 16, kVec, 2>(p, stream);
-  if (p.H <= 2048) return launch_norm_grad_as<T, 128, 16, kVec, 2>(p, stream);
-  if (p.H <= 4096) return launch_norm_grad_as<T, 256, 16, kVec, 2>(p, stream);
-  if (p.H <= 8192) return launch_norm_grad_as<T, 512, 16, kVec, 1>(p, stream);
-  return launch_norm_grad_as<T, 1024, 16, kVec, 1>(p, stream);
+  if (p.H <= 256) return launch_norm_grad_as<T, 32, 8, 8, kVec, 2>(p, stream);
+  if (p.H <= 512) return launch_norm_grad_as<T, 32, 8, 16, kVec, 2>(p, stream);
+  if (p.H <= 1024) return launch_norm_grad_as<T, 64, 4, 16, kVec, 2>(p, stream);
+  if (p.H <= 2048) return launch_norm_grad_as<T, 128, 2, 16, kVec, 2>(p, stream);
+  if (p.H <= 4096) return launch_norm_grad_as<T, 256, 1, 16, kVec, 2>(p, stream);
+  if (p.H <= 8192) return launch_norm_grad_as<T, 512, 1, 16, kVec, 1>(p, stream);
+  return launch_norm_grad_as<T, 1024, 1, 16, kVec, 1>(p, stream);
 }
 
 // ---------------------------------------------------------------- unpack
@@ -686,7 +794,7 @@ strata_status strata_rmsnorm(int dtype, const void *x, long long x_stride, const
 
 size_t strata_rmsnorm_backward_workspace(int n_tokens, int hidden) {
   if (n_tokens < 0 || hidden < 1 || hidden > kNormMaxH) return 0;
-  const size_t blocks = grad_blocks(n_tokens > 0 ? n_tokens : 1);
+  const size_t blocks = grad_blocks(n_tokens > 0 ? n_tokens : 1, hidden);
   return blocks * hidden * sizeof(float);
 }
 
@@ -727,7 +835,7 @@ strata_status strata_rmsnorm_backward(int dtype, const void *h, long long h_stri
   p.eps = eps;
   p.inv_h = (float)(1.0 / hidden);
   const bool vec = hidden % 8 == 0 && rows_vec(h, h_stride, b) && rows_vec(dout, dout_stride, b) &&
-                   rows_vec(dsum, dsum_stride, b) && rows_vec(dx, dx_stride, b);
+                   rows_vec(dsum, dsum_stride, b) && rows_vec(dx, dx_stride, b) && aligned(weight, 16);
   cudaError_t e;
   switch (dtype) {
     case STRATA_DTYPE_BF16:
@@ -742,7 +850,7 @@ strata_status strata_rmsnorm_backward(int dtype, const void *h, long long h_stri
   }
   if (e == cudaSuccess && dweight)
     e = launch_pdl(norm_grad_sum_kernel, dim3((hidden + 31) / 32), dim3(1024), 0, stream,
-                   (const float *)p.partial, grad_blocks(n_tokens), hidden, dweight);
+                   (const float *)p.partial, grad_blocks(n_tokens, hidden), hidden, dweight);
   return status_of(e);
 }
 

@@ -862,10 +862,13 @@ int prep_blocks(int T) {
   return n < 4 * kPairs ? n : 4 * kPairs;
 }
 int h_tiles(int H) { return (H + kTileH - 1) / kTileH; }
-// Pairs of blocks for dW: all of them, as long as each gets a stage.
+// Pairs of blocks for dW: all of them, as long as each gets a stage, and at the
+// most 24 to a tile: every part of a tile is written and read again (8192 tokens
+// x 256 h x 256 experts, whole call: 33.3 us with 74 parts, 30.0 with 24, 31.8
+// with 16).
 int dw_pairs(int T, int H) {
-  const long long units = (long long)h_tiles(H) * ((T + kDwTok - 1) / kDwTok);
-  return units < kPairs ? (int)units : kPairs;
+  const long long tiles = h_tiles(H), n_kb = (T + kDwTok - 1) / kDwTok;
+  return (int)std::min<long long>(kPairs, tiles * std::min<long long>(n_kb, 24));
 }
 
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
