@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import enum
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libstrata_moe.so")
@@ -86,6 +87,11 @@ def load_library():
             "strata_moe_balance_backward": (I, [P, P, I, P, I, P, F, P, P, P, P, P]),
             "strata_moe_route_backward_workspace": (Z, [P, I]),
             "strata_moe_route_backward": (I, [P, P, I, P, P, P, P, P, P, P, P, Z, P]),
+            "strata_packed_rmsnorm": (I, [P]),
+            "strata_packed_rmsnorm_backward": (I, [P]),
+            "strata_packed_balance": (I, [P]),
+            "strata_packed_balance_backward": (I, [P]),
+            "strata_packed_route_backward": (I, [P]),
             "strata_moe_forward_norm": (I, [P, P, P, P, F, I, P, P, P, P]),
             "strata_moe_forward_q8": (I, [P, P, P, I, I, P, P, P]),
             "strata_status_str": (ctypes.c_char_p, [I]),
@@ -265,12 +271,13 @@ def _refuse(where):
     raise StrataError(Status.INVALID_ARG, where)
 
 
-# Operands of the calls that take torch tensors: their addresses, once their
-# sizes, types and device go together (dev: the device index of the first one).
+# Operands of the calls that take torch tensors: their addresses (0: not given),
+# once their sizes, types and device go together (dev: the device index of the
+# first one).
 def _rows(t, shape, dtype, dev, where):
-    """(address, row stride) of a 2-D operand with unit column stride, or (None, 0)."""
+    """(address, row stride) of a 2-D operand with unit column stride."""
     if t is None:
-        return None, 0
+        return 0, 0
     if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
         _refuse(where)
     ld, one = t.stride()
@@ -279,28 +286,53 @@ def _rows(t, shape, dtype, dev, where):
     return t.data_ptr(), ld
 
 
-def _flat(t, dev, n, itemsize, where):
-    """Address of a contiguous operand of n * itemsize bytes, or None."""
+def _flat(t, dev, nbytes, where):
+    """Address of a contiguous operand of nbytes bytes."""
     if t is None:
-        return None
-    if t.nbytes != n * itemsize or t.get_device() != dev or not t.is_contiguous():
+        return 0
+    if t.nbytes != nbytes or t.get_device() != dev or not t.is_contiguous():
         _refuse(where)
     return t.data_ptr()
 
 
 def _workspace(t, dev, where):
-    """(address, bytes) of a workspace, or (None, 0)."""
+    """(address, bytes) of a workspace."""
     if t is None:
-        return None, 0
+        return 0, 0
     if t.get_device() != dev or not t.is_contiguous():
         _refuse(where)
     return t.data_ptr(), t.nbytes
 
 
-def _on_current(dev, where):
-    """A kernel runs on the current device: its operands have to be there."""
-    if dev < 0 or dev != (_torch or _get_torch()).cuda.current_device():
+def _stream_on(stream, dev, where):
+    """Handle of the stream of a call on device dev, which must be the current one."""
+    t = _torch or _get_torch()
+    if dev < 0 or dev != t.cuda.current_device():
         _refuse(where)
+    return t._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+# The arguments of the calls below go to the library as one array of 8-byte
+# words (csrc/packed.cu), which takes a third of the time of converting them
+# one by one.
+class _Packed:
+    def __init__(self, name, words):
+        self.name, self.pack, self.call = name, struct.Struct(words).pack, None
+
+    def __call__(self, where, *words):
+        call = self.call
+        if call is None:
+            call = self.call = getattr(_load(), self.name)
+        st = call(self.pack(*words))
+        if st != 0:
+            raise StrataError(st, where)
+
+
+_packed_rmsnorm = _Packed("strata_packed_rmsnorm", "=6qd10q")
+_packed_rmsnorm_backward = _Packed("strata_packed_rmsnorm_backward", "=4qd12q")
+_packed_balance = _Packed("strata_packed_balance", "=7qd6q")
+_packed_balance_backward = _Packed("strata_packed_balance_backward", "=6qd5q")
+_packed_route_backward = _Packed("strata_packed_route_backward", "=13q")
 
 
 def strata_rmsnorm(x, residual, weight, eps, residual_out=None, out=None, out_q8=None, scales=None,
@@ -315,16 +347,15 @@ def strata_rmsnorm(x, residual, weight, eps, residual_out=None, out=None, out_q8
     ra, ldr = _rows(residual, shape, dt, dev, w)
     roa, ldro = _rows(residual_out, shape, dt, dev, w)
     oa, ldo = _rows(out, shape, dt, dev, w)
-    sa = qa = None
+    sa = qa = 0
     if out_q8 is not None:
         if group <= 0 or scales is None:
             _refuse(w)
-        qa = _flat(out_q8, dev, T * H, 1, w)
-        sa = _flat(scales, dev, T * -(-H // group), 4, w)
-    wa = _flat(weight, dev, H, 4, w)
-    _on_current(dev, w)
-    _check(_load().strata_rmsnorm(_dtype(x), xa, ldx, ra, ldr, wa, eps, T, H, roa, ldro, oa, ldo, qa,
-                                  sa, group, _stream(stream)), w)
+        qa = _flat(out_q8, dev, T * H, w)
+        sa = _flat(scales, dev, T * -(-H // group) * 4, w)
+    wa = _flat(weight, dev, H * 4, w)
+    _packed_rmsnorm(w, _dtype(x), xa, ldx, ra, ldr, wa, eps, T, H, roa, ldro, oa, ldo, qa, sa, group,
+                    _stream_on(stream, dev, w))
 
 
 def strata_rmsnorm_backward_workspace(n_tokens, hidden):
@@ -342,11 +373,10 @@ def strata_rmsnorm_backward(h, weight, eps, dout, dsum, dx, dweight=None, worksp
     da, ldd = _rows(dout, shape, dt, dev, w)
     sa, lds = _rows(dsum, shape, dt, dev, w)
     xa, ldx = _rows(dx, shape, dt, dev, w)
-    wa, dwa = _flat(weight, dev, H, 4, w), _flat(dweight, dev, H, 4, w)
+    wa, dwa = _flat(weight, dev, H * 4, w), _flat(dweight, dev, H * 4, w)
     ws, nws = _workspace(workspace, dev, w)
-    _on_current(dev, w)
-    _check(_load().strata_rmsnorm_backward(_dtype(h), ha, ldh, wa, eps, da, ldd, sa, lds, T, H, xa,
-                                           ldx, dwa, ws, nws, _stream(stream)), w)
+    _packed_rmsnorm_backward(w, _dtype(h), ha, ldh, wa, eps, da, ldd, sa, lds, T, H, xa, ldx, dwa,
+                             ws, nws, _stream_on(stream, dev, w))
 
 
 def strata_moe_forward_norm(h, x, residual, weight, eps, n_tokens, residual_out, normed, out,
@@ -524,21 +554,20 @@ class StrataMoE:
     def forward_norm(self, x, residual, weight, eps, residual_out, normed, out, stream=None):
         w = "strata_moe_forward_norm"
         T, dev = x.shape[0], x.get_device()
-        n = T * self.hidden
-        a = [_flat(t, dev, n, 2, w) for t in (x, residual, residual_out, normed, out)]
-        wa = _flat(weight, dev, self.hidden, 4, w)
-        _on_current(dev, w)
-        strata_moe_forward_norm(self.h, a[0], a[1], wa, eps, T, a[2], a[3], a[4], stream)
+        n = T * self.hidden * 2
+        a = [_flat(t, dev, n, w) for t in (x, residual, residual_out, normed, out)]
+        wa = _flat(weight, dev, self.hidden * 4, w)
+        strata_moe_forward_norm(self.h, a[0], a[1], wa, eps, T, a[2], a[3], a[4],
+                                _stream_on(stream, dev, w))
 
     def forward_q8(self, x_q8, scales, group, x, out, stream=None):
         w = "strata_moe_forward_q8"
         T, H, dev = x_q8.shape[0], self.hidden, x_q8.get_device()
         if group <= 0:
             _refuse(w)
-        qa, sa = _flat(x_q8, dev, T * H, 1, w), _flat(scales, dev, T * -(-H // group), 4, w)
-        xa, oa = _flat(x, dev, T * H, 2, w), _flat(out, dev, T * H, 2, w)
-        _on_current(dev, w)
-        strata_moe_forward_q8(self.h, qa, sa, group, T, xa, oa, stream)
+        qa, sa = _flat(x_q8, dev, T * H, w), _flat(scales, dev, T * -(-H // group) * 4, w)
+        xa, oa = _flat(x, dev, T * H * 2, w), _flat(out, dev, T * H * 2, w)
+        strata_moe_forward_q8(self.h, qa, sa, group, T, xa, oa, _stream_on(stream, dev, w))
 
     # Training the router; `workspace` is a buffer of the size that the
     # *_workspace method gives, kept by the caller.
@@ -550,27 +579,25 @@ class StrataMoE:
         w = "strata_moe_balance"
         T, E, dev = logits.shape[0], self.n_experts, logits.get_device()
         n_seq = 1 if seq_off is None else seq_off.numel() - 1
-        la, ia = _flat(logits, dev, T * E, 4, w), _flat(idx, dev, T * self.top_k, 4, w)
-        ca, ta = _flat(counts, dev, n_seq * E, 4, w), _flat(tokens, dev, n_seq, 4, w)
-        sa, ma = _flat(seq_off, dev, n_seq + 1, 4, w), _flat(mask, dev, T, 1, w)
-        loa = _flat(loss, dev, 1, 4, w)
+        la, ia = _flat(logits, dev, T * E * 4, w), _flat(idx, dev, T * self.top_k * 4, w)
+        ca, ta = _flat(counts, dev, n_seq * E * 4, w), _flat(tokens, dev, n_seq * 4, w)
+        sa, ma = _flat(seq_off, dev, n_seq * 4 + 4, w), _flat(mask, dev, T, w)
+        loa = _flat(loss, dev, 4, w)
         ws, nws = _workspace(workspace, dev, w)
-        _on_current(dev, w)
-        _check(_load().strata_moe_balance(self.h, la, ia, T, sa, n_seq, ma, coef, ca, ta, loa, ws,
-                                          nws, _stream(stream)), w)
+        _packed_balance(w, self.h, la, ia, T, sa, n_seq, ma, coef, ca, ta, loa, ws, nws,
+                        _stream_on(stream, dev, w))
 
     def balance_backward(self, logits, coef, counts, tokens, dlogits, dloss=None, seq_off=None,
                          mask=None, stream=None):
         w = "strata_moe_balance_backward"
         T, E, dev = logits.shape[0], self.n_experts, logits.get_device()
         n_seq = 1 if seq_off is None else seq_off.numel() - 1
-        la, da = _flat(logits, dev, T * E, 4, w), _flat(dlogits, dev, T * E, 4, w)
-        ca, ta = _flat(counts, dev, n_seq * E, 4, w), _flat(tokens, dev, n_seq, 4, w)
-        sa, ma = _flat(seq_off, dev, n_seq + 1, 4, w), _flat(mask, dev, T, 1, w)
-        dla = _flat(dloss, dev, 1, 4, w)
-        _on_current(dev, w)
-        _check(_load().strata_moe_balance_backward(self.h, la, T, sa, n_seq, ma, coef, ca, ta, dla,
-                                                   da, _stream(stream)), w)
+        la, da = _flat(logits, dev, T * E * 4, w), _flat(dlogits, dev, T * E * 4, w)
+        ca, ta = _flat(counts, dev, n_seq * E * 4, w), _flat(tokens, dev, n_seq * 4, w)
+        sa, ma = _flat(seq_off, dev, n_seq * 4 + 4, w), _flat(mask, dev, T, w)
+        dla = _flat(dloss, dev, 4, w)
+        _packed_balance_backward(w, self.h, la, T, sa, n_seq, ma, coef, ca, ta, dla, da,
+                                 _stream_on(stream, dev, w))
 
     def route_backward_workspace(self, n_tokens):
         return strata_moe_route_backward_workspace(self.h, n_tokens)
@@ -579,14 +606,13 @@ class StrataMoE:
         w = "strata_moe_route_backward"
         T, dev = x.shape[0], x.get_device()
         E, k, H = self.n_experts, self.top_k, self.hidden
-        xa, dxa = _flat(x, dev, T * H, 2, w), _flat(dx, dev, T * H, 2, w)
-        la, dla = _flat(logits, dev, T * E, 4, w), _flat(dlogits, dev, T * E, 4, w)
-        ia, dwa = _flat(idx, dev, T * k, 4, w), _flat(dw, dev, T * k, 4, w)
-        dWa, dba = _flat(dW, dev, E * H, 4, w), _flat(db, dev, E, 4, w)
+        xa, dxa = _flat(x, dev, T * H * 2, w), _flat(dx, dev, T * H * 2, w)
+        la, dla = _flat(logits, dev, T * E * 4, w), _flat(dlogits, dev, T * E * 4, w)
+        ia, dwa = _flat(idx, dev, T * k * 4, w), _flat(dw, dev, T * k * 4, w)
+        dWa, dba = _flat(dW, dev, E * H * 4, w), _flat(db, dev, E * 4, w)
         ws, nws = _workspace(workspace, dev, w)
-        _on_current(dev, w)
-        _check(_load().strata_moe_route_backward(self.h, xa, T, la, ia, dwa, dla, dWa, dba, dxa, ws,
-                                                 nws, _stream(stream)), w)
+        _packed_route_backward(w, self.h, xa, T, la, ia, dwa, dla, dWa, dba, dxa, ws, nws,
+                               _stream_on(stream, dev, w))
 
     def status(self, stream=None):
         return strata_moe_get_status(self.h, stream)
