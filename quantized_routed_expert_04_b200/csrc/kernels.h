@@ -156,6 +156,7 @@ struct RouteGradParams {
   int *status;
   // set by run_route_grad (workspace)
   int Epad, tok_blocks;
+  int small_red;           // few tokens: offset of dW's parts in shared memory
   __nv_bfloat16 *dlp;      // [3][T][Epad] bf16 pieces of dl
   __half *dl16;            // [T][Epad] dl / t_scale (up to the scale of W16)
   float *t_scale;          // [T]

@@ -52,9 +52,17 @@ __device__ __forceinline__ uint4 take_bf16(float v[8]) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Over groups of `lanes` (a power of two) lanes.
+__device__ __forceinline__ float group_sum(float v, int lanes) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < lanes) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float group_max(float v, int lanes) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < lanes) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 
@@ -102,29 +110,28 @@ __device__ __forceinline__ void load_selected(const RouteGradParams &p, long lon
   if (sel && in.id >= 0) in.l = p.logits[t * p.E + in.id];
 }
 
-// Lane j: the gradient of selection j's logit through the routing weights.
-__device__ __forceinline__ float weight_grad(const RouteGradParams &p, const TokenIn &in) {
-  const bool use = in.id >= 0;
+// Lane j of a token's group of lanes: the gradient of selection j's logit
+// through the routing weights, from the logit l and dw (id < 0: no selection).
+__device__ __forceinline__ float weight_grad(const RouteMode &mode, int id, float l, float dw, int lanes) {
+  const bool use = id >= 0;
   float w, slope;   // w_j / scale, and its factor in the gradient
-  if (p.mode.sigmoid) {
-    const float ex = expf(-in.l);
+  if (mode.sigmoid) {
+    const float ex = expf(-l);
     const float s = use ? __fdiv_rn(1.0f, 1.0f + ex) : 0.0f;
-    const float z = warp_sum(s);
+    const float z = group_sum(s, lanes);
     // (a true division: one selected expert has w = 1 and no gradient)
     w = z == 0.0f ? 0.0f : __fdiv_rn(s, z);
-    slope = s == 0.0f ? 0.0f : p.mode.scale * w * (ex * s);
+    slope = s == 0.0f ? 0.0f : mode.scale * w * (ex * s);
   } else {
-    float m = use ? in.l : __int_as_float(0xff800000);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float m = group_max(use ? l : __int_as_float(0xff800000), lanes);
     const bool none = m == __int_as_float(0xff800000);
-    const float ex = !use || (none && in.l == m) ? 0.0f : expf(in.l - m);
-    const float z = warp_sum(ex);
+    const float ex = !use || (none && l == m) ? 0.0f : expf(l - m);
+    const float z = group_sum(ex, lanes);
     w = z == 0.0f ? 0.0f : __fdiv_rn(ex, z);
     slope = w;
   }
-  const float dot = warp_sum(use ? w * in.dw : 0.0f);
-  return use ? slope * (in.dw - dot) : 0.0f;
+  const float dot = group_sum(use ? w * dw : 0.0f, lanes);
+  return use ? slope * (dw - dot) : 0.0f;
 }
 
 // Eight floats -> f16.
@@ -172,7 +179,7 @@ __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const 
     if (p.dw) {
       // scattered through a row of shared memory that is zero in between; of
       // lanes with the same expert the first adds up all, in lane order
-      float g = weight_grad(p, in);
+      float g = weight_grad(p.mode, in.id, in.l, in.dw, 32);
       const unsigned same = __match_any_sync(0xffffffffu, in.id);
       const bool first = (same & ((1u << lane) - 1u)) == 0u && in.id >= 0;
       if (__any_sync(0xffffffffu, in.id >= 0 && (same & (same - 1u)) != 0u)) {
@@ -853,6 +860,198 @@ __global__ void __launch_bounds__(kDxThreads, 1)
   pair_end(s, warp);
 }
 
+// ---------------------------------------------------------------- few tokens
+// The whole of it in one launch on the fp32 units: a block per 16 or 32 h computes dl
+// (every block the same) into shared memory and takes its columns of dW and dx.  The three launches of the other form take 11 to 18 us however small the
+// batch is; this one takes 5 us with one token, 10.8 with 129 tokens x 64 experts
+// x 2048 (13.7).
+constexpr int kSmallThreads = 1024;
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(void *dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// Threads that share a tile of dW (four experts x one h; n tiles).
+__host__ __device__ inline int small_parts(int n) {
+  int parts = 1;
+  while (parts < 16 && 2 * parts * n <= kSmallThreads) parts *= 2;
+  return parts;
+}
+// Shared memory: dl [T][Ep] and W [Ep][hs] in fp32, x [T][hs] in bf16, the parts
+// of dW; Ep: the experts rounded up to four.
+struct SmallSmem {
+  size_t red, total;
+};
+// h a block: 16, or 32 where that would be more blocks than multiprocessors.
+inline int small_hs(int H) { return H / 16 > 148 ? 32 : 16; }
+SmallSmem small_smem(int T, int E, int H) {
+  const int hs = small_hs(H);
+  const size_t Ep = (E + 3) / 4 * 4;
+  const int n = (int)Ep / 4 * hs, parts = small_parts(n);
+  const size_t red = 4 * (T * Ep + Ep * hs) + (size_t)2 * T * hs;
+  return {red, red + (parts > 1 ? (size_t)n * parts * 16 : 0)};
+}
+
+template <int kSmallH>
+__global__ void __launch_bounds__(kSmallThreads) route_grad_small_kernel(const RouteGradParams p) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  grid_dependency_wait();
+  grid_dependency_launch();
+  const int T = p.T, E = p.E, k = p.k, H = p.H, Ep = (E + 3) & ~3;
+  float *dl = reinterpret_cast<float *>(smem_raw);
+  float *ws = dl + (size_t)T * Ep;
+  __nv_bfloat16 *xs = reinterpret_cast<__nv_bfloat16 *>(ws + Ep * kSmallH);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h0 = blockIdx.x * kSmallH;
+  // everything that is read as it is, in flight at once
+  if (p.dlogits && Ep == E && (reinterpret_cast<uintptr_t>(p.dlogits) & 15) == 0) {
+    for (int i = tid; i < T * E / 4; i += kSmallThreads) cp_async16(dl + 4 * i, p.dlogits + 4 * i);
+  } else {
+    for (int t = warp; t < T; t += kSmallThreads / 32)
+      for (int e = lane; e < Ep; e += 32) {
+        if (p.dlogits && e < E)
+          cp_async4(dl + t * Ep + e, p.dlogits + (size_t)t * E + e);
+        else
+          dl[t * Ep + e] = 0.0f;
+      }
+  }
+  if (p.dW)
+    for (int i = tid; i < T * (kSmallH / 8); i += kSmallThreads)
+      cp_async16(xs + 8 * i, p.x + (size_t)(i / (kSmallH / 8)) * H + h0 + 8 * (i % (kSmallH / 8)));
+  if (p.dx)
+    for (int i = tid; i < Ep * (kSmallH / 4); i += kSmallThreads) {
+      const int e = i / (kSmallH / 4);
+      if (e < E)
+        cp_async16(ws + 4 * i, p.W + (size_t)e * H + h0 + 4 * (i % (kSmallH / 4)));
+      else
+        *reinterpret_cast<float4 *>(ws + 4 * i) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  // meanwhile the gradient through the routing weights: a group of lanes (the
+  // power of two that holds k) per token
+  int lanes = 1;
+  while (lanes < k) lanes *= 2;
+  const int at_once = kSmallThreads / lanes;
+  bool met = false;
+  auto meet = [&] {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    met = true;
+  };
+  if (p.dw) {
+    const int j = lane & (lanes - 1);
+    const unsigned group = (lanes == 32 ? 0xffffffffu : (1u << lanes) - 1u) << (lane - j);
+    for (int t0 = 0; t0 < T; t0 += at_once) {
+      const int t = t0 + tid / lanes;
+      const bool sel = t < T && j < k;
+      int id = sel ? p.idx[(size_t)t * k + j] : -1;
+      const float dw = sel ? p.dw[(size_t)t * k + j] : 0.0f;
+      const bool bad = sel && (id < 0 || id >= E);
+      if (bad) set_status(p.status, STATUS_BAD_ROUTING);
+      if (__ballot_sync(0xffffffffu, bad) & group) id = -1;   // (as the other form)
+      const float l = id >= 0 ? p.logits[(size_t)t * E + id] : 0.0f;
+      const float g = weight_grad(p.mode, id, l, dw, lanes);
+      // of lanes of the token with the same expert the first adds up all
+      float sum = 0.0f;
+      bool first = id >= 0;
+      for (int q = 0; q < k; ++q) {
+        const int from = lane - j + q;
+        const int other = __shfl_sync(0xffffffffu, id, from);
+        const float og = __shfl_sync(0xffffffffu, g, from);
+        if (other == id) {
+          sum += og;
+          first = first && q >= j;
+        }
+      }
+      if (!met) meet();
+      if (first) dl[t * Ep + id] += sum;
+    }
+  }
+  if (!met) meet();
+  __syncthreads();
+  if (p.dx) {   // (the limit of the other form: what is refused does not go by the batch)
+    bool over = false;
+    for (int i = tid; i < E * kSmallH; i += kSmallThreads) over |= fabsf(ws[i]) * kWScale >= kF16Overflow;
+    if (over) set_status(p.status, STATUS_RANGE);
+  }
+  // dW: four experts of one h a thread; where that leaves threads over, the
+  // tokens are split between up to 16 of them, whose sums meet below
+  const int n = Ep / 4 * kSmallH, parts = small_parts(n);
+  float4 *red = reinterpret_cast<float4 *>(smem_raw + p.small_red);   // [parts][n]
+  auto put = [&](int tile, const float4 &a) {
+    const int h = tile % kSmallH, e = tile / kSmallH * 4;
+    float *out = p.dW + (size_t)e * H + h0 + h;
+    out[0] = a.x;
+    if (e + 1 < E) out[H] = a.y;
+    if (e + 2 < E) out[2 * (size_t)H] = a.z;
+    if (e + 3 < E) out[3 * (size_t)H] = a.w;
+  };
+  if (p.dW) {
+    for (int q = tid; q < n * parts; q += kSmallThreads) {
+      const int part = q / n, tile = q - part * n;
+      const int h = tile % kSmallH, e = tile / kSmallH * 4;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int t = part; t < T; t += parts) {
+        const float4 d = *reinterpret_cast<const float4 *>(dl + t * Ep + e);
+        const float x = __bfloat162float(xs[t * kSmallH + h]);
+        a.x = fmaf(d.x, x, a.x);
+        a.y = fmaf(d.y, x, a.y);
+        a.z = fmaf(d.z, x, a.z);
+        a.w = fmaf(d.w, x, a.w);
+      }
+      if (parts == 1)
+        put(tile, a);
+      else
+        red[q] = a;
+    }
+  }
+  // dx: two h of a token a thread (the threads in reverse, so that those without
+  // a part of dW go first)
+  if (p.dx) {
+    for (int q = kSmallThreads - 1 - tid; q < T * (kSmallH / 2); q += kSmallThreads) {
+      const int h = q % (kSmallH / 2) * 2, t = q / (kSmallH / 2);
+      float a0 = 0.0f, a1 = 0.0f;
+#pragma unroll 2
+      for (int e = 0; e < Ep; e += 4) {
+        const float4 d = *reinterpret_cast<const float4 *>(dl + t * Ep + e);
+        const float dv[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 w = *reinterpret_cast<const float2 *>(ws + (e + i) * kSmallH + h);
+          a0 = fmaf(dv[i], w.x, a0);
+          a1 = fmaf(dv[i], w.y, a1);
+        }
+      }
+      *reinterpret_cast<__nv_bfloat162 *>(p.dx + (size_t)t * H + h0 + h) = __floats2bfloat162_rn(a0, a1);
+    }
+  }
+  if (p.dW && parts > 1) {
+    __syncthreads();
+    for (int tile = tid; tile < n; tile += kSmallThreads) {
+      float4 a = red[tile];
+      for (int part = 1; part < parts; ++part) {
+        const float4 v = red[part * n + tile];
+        a.x += v.x;
+        a.y += v.y;
+        a.z += v.z;
+        a.w += v.w;
+      }
+      put(tile, a);
+    }
+  }
+  // db: a warp per expert, the experts spread over the blocks
+  if (p.db)
+    for (int e = blockIdx.x + gridDim.x * warp; e < E; e += gridDim.x * (kSmallThreads / 32)) {
+      float v = 0.0f;
+      for (int t = lane; t < T; t += 32) v += dl[t * Ep + e];
+      v = group_sum(v, 32);
+      if (lane == 0) p.db[e] = v;
+    }
+}
+
 // ---------------------------------------------------------------- host
 constexpr int kPairs = 74;   // 148 multiprocessors
 static_assert(4 * kPairs <= 320, "sum_db reads up to 320 blocks' parts");
@@ -915,7 +1114,24 @@ bool encode_planes(CUtensorMap *m, CUtensorMapDataType type, const void *base, i
 
 size_t route_grad_workspace(int T, int E, int H) { return layout(T > 0 ? T : 1, E, H).total; }
 
+// One launch on the fp32 units while the products of a block stay few: it takes
+// about 5.5 us + 0.042 us per 1024 of them, the other form 11 (8 experts) to 18
+// us (256) before its products count.  E.g. 64 experts x 2048 h: 10.8 against
+// 13.7 us with 128 tokens, 17.7 against 14.2 with 256; 256 experts x 1024: 10.1
+// against 18.5 with 32, 25.9 against 19.0 with 128.  (At most 40 KB of dl, 80 of
+// x, 32 of W and 16 of parts in shared memory.)
+bool few_tokens(int T, int E, int H) { return (long long)T * ((E + 3) / 4 * 4) * small_hs(H) <= 160 * 1024; }
+
 cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stream) {
+  if (few_tokens(p.T, p.E, p.H)) {
+    const SmallSmem layout = small_smem(p.T, p.E, p.H);
+    const int smem = (int)layout.total, hs = small_hs(p.H);
+    p.small_red = (int)layout.red;
+    auto kern = hs == 16 ? route_grad_small_kernel<16> : route_grad_small_kernel<32>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(p.H / hs), dim3(kSmallThreads), smem, stream, p);
+  }
   const Layout L = layout(p.T, p.E, p.H);
   char *w = static_cast<char *>(workspace);
   p.Epad = (p.E + 7) / 8 * 8;

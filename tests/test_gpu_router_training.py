@@ -378,7 +378,10 @@ def acts(T, H, seed):
 
 SHAPES = [(1, 128, 1, 1), (1, 256, 8, 2), (2, 128, 64, 6), (31, 384, 60, 6), (33, 256, 100, 5),
           (64, 512, 16, 1), (129, 2048, 64, 6), (127, 256, 255, 10), (128, 128, 256, 8),
-          (257, 640, 256, 32), (1000, 1152, 160, 4), (2048, 4096, 32, 8), (4099, 512, 129, 3)]
+          (257, 640, 256, 32), (1000, 1152, 160, 4), (2048, 4096, 32, 8), (4099, 512, 129, 3),
+          # few tokens (one launch) and just beyond, 16 and 32 h a block
+          (40, 512, 255, 8), (41, 512, 256, 8), (19, 4096, 256, 10), (25, 4096, 256, 10),
+          (160, 2048, 64, 6), (161, 2048, 64, 6), (1280, 256, 7, 2), (1281, 256, 8, 1)]
 
 
 @pytest.mark.parametrize("mode", ["softmax", "sigmoid"])
