@@ -350,6 +350,10 @@ __global__ void __launch_bounds__(kTpr *kRows) norm_kernel(const NormParams p) {
   }
 }
 
+// Threads per row: 16 elements each at the widths where a row has the threads to
+// itself (8192 x 4096 bf16 with residual and 8-bit output: 49.5 us with 256
+// threads, 50.3 with 128 of 32 elements, 51.8 with 512 of 8), fewer on short
+// rows, where a warp has one.
 template <typename T, bool kVec>
 cudaError_t launch_norm(const NormParams &p, cudaStream_t stream) {
   const int H = p.H, T_ = p.T;
@@ -745,6 +749,7 @@ strata_status strata_rmsnorm(int dtype, const void *x, long long x_stride, const
   if (!b || n_tokens < 0 || hidden < 1 || !(eps >= 0.0f) || !(eps <= 3.0e38f))
     return STRATA_ERR_INVALID_ARG;
   if (hidden > kNormMaxH) return STRATA_ERR_UNSUPPORTED;
+  if (residual_out && residual_out == out) return STRATA_ERR_INVALID_ARG;
   if (out_q8 ? !scales || (group != 32 && group != 64 && group != 128 && group < hidden)
              : scales != nullptr)
     return STRATA_ERR_INVALID_ARG;

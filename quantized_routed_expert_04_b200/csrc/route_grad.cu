@@ -445,7 +445,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int la
 //   form 0, up to 64 experts:   one MMA: hi 64 | mid 64 | lo 64 | (not used)
 //   form 1, up to 128 experts:  two: hi 128 | mid 128, then lo 128 on top of hi
 //   form 2, up to 256 experts:  three: hi, mid, lo, 256 columns each
-// and the epilogue adds the columns of an expert.
+// and the epilogue adds the columns of an expert.  Whole calls over 4096 h, in
+// form 2 and in their own: 32 experts x 2048 tokens 28.6 and 22.5 us, 128 experts
+// 32.2 and 26.7, 64 experts x 8192 tokens 64.3 and 52.5.
 constexpr int kDwTok = 32;
 constexpr int kDwBox = kDwTok * 128;   // 64 columns
 template <int kForm>

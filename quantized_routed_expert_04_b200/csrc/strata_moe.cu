@@ -896,7 +896,8 @@ strata_status strata_moe_balance_backward(strata_moe *h, const float *logits, in
   strata_status st = check_balance(h, logits, n_tokens, seq_off, n_seq, coef, counts, tokens);
   if (st != STRATA_OK) return st;
   if (misaligned(dloss, 4)) return STRATA_ERR_INVALID_ARG;
-  if (n_tokens > 0 && (!dlogits || misaligned(dlogits, 4))) return STRATA_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (!dlogits || misaligned(dlogits, 4) || dlogits == logits))
+    return STRATA_ERR_INVALID_ARG;
   st = check_device(h);
   if (st != STRATA_OK) return st;
   if (n_tokens == 0) return STRATA_OK;

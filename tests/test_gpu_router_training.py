@@ -289,7 +289,7 @@ def test_balance_refusals():
         assert call(**kw) == int(BAD), kw
     d = torch.zeros(T, E, device="cuda")
     for kw in (dict(counts=c[:7]), dict(tokens=c), dict(dlogits=d[:, :7]), dict(mask=c),
-               dict(logits=logits.cpu())):
+               dict(logits=logits.cpu()), dict(dlogits=logits)):
         a = {**dict(logits=logits, coef=0.1, counts=c, tokens=t, dlogits=d), **kw}
         with pytest.raises(binding.StrataError):
             layer.balance_backward(**a)

@@ -6,7 +6,8 @@ from quantized_routed_expert_04_b200 import binding, build
 
 BAD, UNSUP, OK = (int(binding.Status.INVALID_ARG), int(binding.Status.UNSUPPORTED),
                   int(binding.Status.OK))
-P = 1 << 20   # an aligned address that is never read
+P = 1 << 20   # aligned addresses that are never read
+Q = 1 << 21
 
 
 @pytest.fixture(scope="module")
@@ -15,7 +16,7 @@ def lib():
     return binding.load_library()
 
 
-def fwd(lib, dtype=0, x=P, ldx=256, r=P, ldr=256, w=P, eps=1e-6, T=4, H=256, ro=P, ldro=256, out=P,
+def fwd(lib, dtype=0, x=P, ldx=256, r=P, ldr=256, w=P, eps=1e-6, T=4, H=256, ro=P, ldro=256, out=Q,
         ldo=256, q8=None, sc=None, group=0):
     return lib.strata_rmsnorm(dtype, x, ldx, r, ldr, w, eps, T, H, ro, ldro, out, ldo, q8, sc,
                               group, None)
@@ -25,7 +26,7 @@ def fwd(lib, dtype=0, x=P, ldx=256, r=P, ldr=256, w=P, eps=1e-6, T=4, H=256, ro=
     dict(dtype=3), dict(dtype=-1), dict(x=None), dict(w=None), dict(out=None), dict(T=-1),
     dict(H=0), dict(eps=-1e-6), dict(eps=float("nan")), dict(eps=float("inf")), dict(ldx=255),
     dict(ldr=255), dict(ldro=0), dict(ldo=-256), dict(x=P + 1), dict(r=P + 1), dict(ro=P + 1),
-    dict(out=P + 1), dict(w=P + 2), dict(q8=P, sc=None, group=32), dict(q8=None, sc=P),
+    dict(out=P + 1), dict(w=P + 2), dict(ro=Q, out=Q), dict(q8=P, sc=None, group=32), dict(q8=None, sc=P),
     dict(q8=P, sc=P, group=0), dict(q8=P, sc=P, group=96), dict(q8=P, sc=P, group=-32),
     dict(q8=P, sc=P + 2, group=32), dict(dtype=2, x=P + 2),
 ])
