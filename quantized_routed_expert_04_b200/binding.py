@@ -304,6 +304,11 @@ def _workspace(t, dev, where):
     return t.data_ptr(), t.nbytes
 
 
+def _bf16(t, where):
+    if t is not None and t.dtype is not (_torch or _get_torch()).bfloat16:
+        _refuse(where)
+
+
 def _stream_on(stream, dev, where):
     """Handle of the stream of a call on device dev, which must be the current one."""
     t = _torch or _get_torch()
@@ -553,6 +558,7 @@ class StrataMoE:
     # (StrataError, INVALID_ARG).
     def forward_norm(self, x, residual, weight, eps, residual_out, normed, out, stream=None):
         w = "strata_moe_forward_norm"
+        _bf16(x, w)
         T, dev = x.shape[0], x.get_device()
         n = T * self.hidden * 2
         a = [_flat(t, dev, n, w) for t in (x, residual, residual_out, normed, out)]
@@ -604,6 +610,8 @@ class StrataMoE:
 
     def route_backward(self, x, logits, idx, dw, dlogits, dW, db, dx, workspace, stream=None):
         w = "strata_moe_route_backward"
+        _bf16(x, w)
+        _bf16(dx, w)
         T, dev = x.shape[0], x.get_device()
         E, k, H = self.n_experts, self.top_k, self.hidden
         xa, dxa = _flat(x, dev, T * H * 2, w), _flat(dx, dev, T * H * 2, w)

@@ -502,6 +502,10 @@ def test_route_backward_no_tokens_and_refusals():
                dict(ws=None), dict(n=need - 1), dict(ws=ws.data_ptr() + 16),
                dict(x=x.data_ptr() + 2), dict(dx=dx.data_ptr() + 2), dict(dW=dW.data_ptr() + 4)):
         assert call(**kw) == int(BAD), kw
+    with pytest.raises(binding.StrataError):   # another 16-bit type
+        layer.route_backward(x.half(), logits, idx, dw, dlg, dW, db, dx, ws)
+    with pytest.raises(binding.StrataError):   # not on the device
+        layer.route_backward(x.cpu(), logits, idx, dw, dlg, dW, db, dx, ws)
     bare = make_layer(E, k, H=H)   # no router set: dx cannot be had, the others can
     assert call(h=bare.h) == int(BAD)
     assert call(h=bare.h, dx=None) == 0
