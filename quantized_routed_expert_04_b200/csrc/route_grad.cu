@@ -708,6 +708,7 @@ constexpr int kDxThreads = 32 * (2 + kDxEpiWarps + kSumWarps);
 
 struct DxParams {
   int T, H, E, stages;
+  int after_dw;           // the kernel before this one on the stream is dW's
   const float *t_scale;   // [T]
   int *status;
 };
@@ -728,8 +729,14 @@ __global__ void __launch_bounds__(kDxThreads, 1)
   }
   pair_begin(s, p.stages, kDxEpiWarps, warp);
   const uint32_t tmem = s.tmem, rank = cluster_rank();
-  grid_dependency_wait();
-  grid_dependency_launch();
+  // dx needs what the preparation wrote, and the dW kernel lets this grid start
+  // only once all its blocks have seen the preparation complete: only the warps
+  // that add up dW's parts wait for the dW kernel itself, so that dx runs beside
+  // it wherever multiprocessors are free.
+  if (!p.after_dw || warp >= 2 + kDxEpiWarps) {
+    grid_dependency_wait();
+    grid_dependency_launch();
+  }
 
   const int n_kb = (p.E + 63) / 64;
   const int t_tiles = (p.T + kDxTok - 1) / kDxTok;
@@ -1177,8 +1184,8 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
         !encode_planes(&mo, kBf16, p.dx, p.H, p.T, p.H, 1, 32))
       return cudaErrorInvalidValue;
     const int fixed = (p.E + 63) / 64 * 2 * kDxWBox + kDxEpiWarps * kDxOut;
-    DxParams d{p.T, p.H, p.E, std::min(kMaxStages, (kSmemLimit - 2048 - fixed) / kDxStage), p.t_scale,
-               p.status};
+    DxParams d{p.T, p.H, p.E, std::min(kMaxStages, (kSmemLimit - 2048 - fixed) / kDxStage),
+               p.dW ? 1 : 0, p.t_scale, p.status};
     const int smem = fixed + d.stages * kDxStage + 1024;
     const long long items = (long long)((p.T + kDxTok - 1) / kDxTok) * tiles;
     // (pairs without an item of dx help with the sums: a row of 256 per warp)
