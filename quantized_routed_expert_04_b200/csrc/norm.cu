@@ -386,9 +386,11 @@ struct NormGradParams {
 // filled by bulk copies, so that several rows of all three inputs are in flight
 // while one is reduced: on 8192 rows of 4096 bf16 with a direct gradient, plain
 // loads with one row ahead in registers took 98 us (waiting for loads; and 88
-// through the ring with elements converted one by one), now 49 us.  The barrier
+// through the ring with elements converted one by one), now 47 us.  The barrier
 // of the row's reduction also frees its stage: every thread has its elements in
-// registers by then.  Without kVec (rows that 16-byte copies cannot walk) the
+// registers by then.  A copy that does not arrive within the limit of its wait
+// ends the copies; its row and all the thread's rows behind it become NaN, and
+// with them the weight's gradient.  Without kVec (rows that 16-byte copies cannot walk) the
 // next row's elements are loaded into registers ahead.
 template <typename T, int kTpr, int kRows, int kNe, bool kVec, int kMinBlocks>
 __global__ void __launch_bounds__(kTpr *kRows, kMinBlocks) norm_grad_kernel(const NormGradParams p) {
@@ -476,6 +478,7 @@ __global__ void __launch_bounds__(kTpr *kRows, kMinBlocks) norm_grad_kernel(cons
   };
   int flip = 0, st = 0;
   uint32_t phase = 0;
+  bool lost = false;   // (every thread takes every step all the same: no barrier is missed)
   for (long long row = row0; row < p.T; row += step, flip ^= 1) {
     float a[kHold ? kNe : 8], d[kHold ? kNe : 8];
     Vec8<T> sc[kVec && kHold ? kNe / 8 : 1];
@@ -492,7 +495,7 @@ __global__ void __launch_bounds__(kTpr *kRows, kMinBlocks) norm_grad_kernel(cons
       }
     };
     if (kVec) {
-      if (!mbar_wait(&full[st], phase, nullptr)) break;
+      lost = lost || !mbar_wait(&full[st], phase, nullptr);
 #pragma unroll
       for (int i = 0; i < kNe; i += 8) {
         unpack_at(i, a + (kHold ? i : 0), d + (kHold ? i : 0));
@@ -529,6 +532,7 @@ __global__ void __launch_bounds__(kTpr *kRows, kMinBlocks) norm_grad_kernel(cons
         dot = fmaf(d[i] * weight(i), a[i], dot);
       }
     }
+    if (kVec && lost) sq = __int_as_float(0x7fffffff);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       sq += __shfl_xor_sync(0xffffffffu, sq, o);
@@ -538,7 +542,7 @@ __global__ void __launch_bounds__(kTpr *kRows, kMinBlocks) norm_grad_kernel(cons
     if (kWarps > 1 && (tid & 31) == 0) s_red[group][flip][tid >> 5] = make_float2(sq, dot);
     if (kWarps > 1 || kVec) meet();
     auto next_stage = [&] {
-      if (tid == 0) fetch(row + p.stages * step, st);
+      if (tid == 0 && !lost) fetch(row + p.stages * step, st);
       if (++st == p.stages) {
         st = 0;
         phase ^= 1u;
