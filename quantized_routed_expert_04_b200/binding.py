@@ -558,7 +558,8 @@ class StrataMoE:
     # (StrataError, INVALID_ARG).
     def forward_norm(self, x, residual, weight, eps, residual_out, normed, out, stream=None):
         w = "strata_moe_forward_norm"
-        _bf16(x, w)
+        for t in (x, residual, residual_out, normed, out):
+            _bf16(t, w)
         T, dev = x.shape[0], x.get_device()
         n = T * self.hidden * 2
         a = [_flat(t, dev, n, w) for t in (x, residual, residual_out, normed, out)]
@@ -569,6 +570,8 @@ class StrataMoE:
     def forward_q8(self, x_q8, scales, group, x, out, stream=None):
         w = "strata_moe_forward_q8"
         T, H, dev = x_q8.shape[0], self.hidden, x_q8.get_device()
+        _bf16(x, w)
+        _bf16(out, w)
         if group <= 0:
             _refuse(w)
         qa, sa = _flat(x_q8, dev, T * H, w), _flat(scales, dev, T * -(-H // group) * 4, w)

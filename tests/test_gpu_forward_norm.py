@@ -125,3 +125,21 @@ def test_refusals(gl):
         gl.layer.forward_norm(x, r[:3], w, EPS, None, n, o)
     with pytest.raises(binding.StrataError):
         gl.layer.forward_q8(q, sc[:3], 32, n, o)
+
+
+def test_types_are_checked(gl):
+    # 16-bit operands of another type than the layer's
+    T, H = 4, gl.cfg.hidden
+    x, r, w = inputs(T, H, 42)
+    s, n, o = (torch.empty_like(x) for _ in range(3))
+    args = [x, r, w, EPS, s, n, o]
+    for i in (0, 1, 4, 5, 6):
+        bad = list(args)
+        bad[i] = bad[i].half()
+        with pytest.raises(binding.StrataError):
+            gl.layer.forward_norm(*bad)
+    q = torch.zeros(T, H, dtype=torch.uint8, device="cuda")
+    sc = torch.ones(T, H // 32, device="cuda")
+    for a, b in ((n.half(), o), (n, o.half())):
+        with pytest.raises(binding.StrataError):
+            gl.layer.forward_q8(q, sc, 32, a, b)
