@@ -396,8 +396,8 @@ enum { STRATA_DTYPE_BF16 = 0, STRATA_DTYPE_F16 = 1, STRATA_DTYPE_F32 = 2 };
  * out_q8 (or NULL): device e4m3 [n_tokens][hidden], contiguous, with one fp32
  * scale per `group` consecutive columns of a row, scales [n_tokens]
  * [ceil(hidden / group)]: scale = max(largest |y| of the group / 448, 2^-126),
- * q = e4m3(y / scale) (nearest even); y is the fp32 value, not the rounded
- * out.  group: 32, 64, 128, or >= hidden for one scale a row.  A group that
+ * q = e4m3(y * (1 / scale)) (1 / scale and the product in fp32, then nearest
+ * even); y is the fp32 value, not the rounded out.  group: 32, 64, 128, or >= hidden for one scale a row.  A group that
  * holds a NaN gets a NaN scale.
  * 16-byte aligned rows of a multiple of 8 elements are fastest; any element
  * alignment works.  Runs on the current device, asynchronous on `stream`; no
@@ -478,7 +478,8 @@ strata_status strata_moe_forward_q8(strata_moe *h, const void *x_q8, const float
  *     loss = coef / n_seq * sum_b sum_e (counts[b][e] n_experts / (top_k n_b))
  *                                       * (sum_t p[t][e] / n_b)
  * A sequence with no counting token adds nothing; a row of logits that are all
- * -inf has no probabilities (zeros).  counts: device int32 [n_seq][n_experts];
+ * -inf has no probabilities (zeros), and a sigmoid score below 2^-126 (a logit
+ * below -87) counts as zero.  counts: device int32 [n_seq][n_experts];
  * tokens: device int32 [n_seq], the n_b; loss: device fp32 [1].  Sums are taken
  * in fp32 within a block of tokens and in double across blocks, in a fixed
  * order.  n_tokens == 0 zeroes the outputs.  Asynchronous on `stream`.

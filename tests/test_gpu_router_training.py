@@ -610,6 +610,94 @@ def test_streams_and_graphs():
     layer.close()
 
 
+@pytest.mark.parametrize("T,H,E,k", [(2700, 256, 40, 4), (1500, 2048, 120, 6), (2300, 1024, 250, 8)])
+def test_route_backward_calls_in_a_row_share_a_workspace(T, H, E, k):
+    # in stream order and without a wait between them, every call writes over what
+    # the one before it read
+    W = router(E, H, 121)
+    layer = make_layer(E, k, "softmax", H, W)
+    cases, want = [], []
+    for seed in (122, 132, 142):
+        logits, idx = routing(T, E, k, seed)
+        cases.append((acts(T, H, seed + 1), logits, idx,
+                      torch.randn(T, k, device="cuda", generator=gen(seed + 2)),
+                      torch.randn(T, E, device="cuda", generator=gen(seed + 3)) * 10.0 ** (seed - 132)))
+        want.append(run_route_backward(layer, *cases[-1]))
+    ws = torch.empty(layer.route_backward_workspace(T), dtype=torch.uint8, device="cuda")
+    got = []
+    for i in range(24):
+        out = (torch.empty(E, H, device="cuda"), torch.empty(E, device="cuda"),
+               torch.empty(T, H, dtype=torch.bfloat16, device="cuda"))
+        layer.route_backward(*cases[i % 3], *out, ws)
+        got.append(out)
+    torch.cuda.synchronize()
+    for i, out in enumerate(got):
+        for n, t in zip(("dW", "db", "dx"), out):
+            assert torch.equal(t, want[i % 3][n]), (i, n)
+    assert int(layer.status()[0]) == 0
+    layer.close()
+
+
+# rows of fewer experts than one 16-byte access, past the few tokens of one launch
+@pytest.mark.parametrize("T,H,E,k", [(10300, 128, 1, 1), (2600, 256, 3, 2), (1300, 384, 5, 5),
+                                     (1290, 512, 7, 1)])
+def test_route_backward_few_experts(T, H, E, k):
+    W, x = router(E, H, 151), acts(T, H, 152)
+    layer = make_layer(E, k, "sigmoid", H, W)
+    logits, idx = routing(T, E, k, 153)
+    dw = torch.randn(T, k, device="cuda", generator=gen(154))
+    dlg = torch.randn(T, E, device="cuda", generator=gen(155)) * 0.05
+    check_route_backward(layer, x, W, logits, idx, dw, dlg, "sigmoid")
+    layer.close()
+
+
+def test_offsets_past_32_bits():
+    # more than 2^31 logits (2^33 bytes); what is checked in detail lies behind them
+    T, H, E, k, n, coef = 2 ** 23 + 1003, 128, 256, 2, 1000, 0.5
+    W = router(E, H, 161)
+    layer = make_layer(E, k, "softmax", H, W)
+    logits = torch.randn(T, E, device="cuda", generator=gen(162))
+    t = torch.arange(T, device="cuda", dtype=torch.int32)
+    idx = torch.stack((t % 251, (t + 3) % 256), 1).contiguous()
+    counts, tokens = (torch.empty(m, dtype=torch.int32, device="cuda") for m in (E, 1))
+    loss, d = torch.empty(1, device="cuda"), torch.empty(T, E, device="cuda")
+    ws = torch.empty(layer.balance_workspace(T), dtype=torch.uint8, device="cuda")
+    layer.balance(logits, idx, coef, counts, tokens, loss, ws)
+    layer.balance_backward(logits, coef, counts, tokens, d)
+    assert int(tokens) == T
+    assert torch.equal(counts.long(), torch.bincount(idx.view(-1).long(), minlength=E))
+    f = counts.double() * E / (k * T)
+    P = sum(torch.softmax(c.double(), 1).sum(0) for c in logits.split(2 ** 18)) / T
+    # (a warp's own share: up to 1800 rows one by one)
+    want = float(coef * (f * P).sum())
+    assert abs(float(loss) - want) <= (1800 + 128) * U * want
+    p = torch.softmax(logits[-n:].double(), 1)
+    dot = (p * f).sum(1, keepdim=True)
+    err = (d[-n:].double() - coef / T * p * (f - dot)).abs()
+    assert bool((err <= coef / T * p * (f + dot) * 128 * U + 2.0 ** -140).all())
+
+    # the router: only the last n tokens have gradients, so dW and db are sums
+    # over those n, and dx is zero in front of them
+    d[:-n] = 0
+    d[-n:] = torch.randn(n, E, device="cuda", generator=gen(163)) * 0.1
+    dw = torch.zeros(T, k, device="cuda")
+    dw[-n:] = torch.randn(n, k, device="cuda", generator=gen(164))
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    x[-n:] = acts(n, H, 165)
+    out = run_route_backward(layer, x, logits, idx, dw, d)
+    assert int(layer.status()[0]) == 0
+    dl, mag = exact_dl(logits[-n:], idx[-n:], dw[-n:], d[-n:], "softmax")
+    xd = x[-n:].double()
+    for got, want, tol in (
+            (out["dW"], dl.t() @ xd, (dl.abs().t() @ xd.abs()) * (3 * n / 8 + 64) * U + (mag.t() @ xd.abs()) * 32 * U),
+            (out["db"], dl.sum(0), dl.abs().sum(0) * (n / 8 + 64) * U + mag.sum(0) * 32 * U),
+            (out["dx"][-n:], dl @ W.double(), dx_rounding(dl, W) + (mag @ W.double().abs()) * 32 * U +
+             (dl @ W.double()).abs() * 2.0 ** -8)):
+        assert bool(((got.double() - want).abs() <= tol + 1e-38).all())
+    assert not bool(out["dx"][:-n].any())
+    layer.close()
+
+
 @pytest.mark.parametrize("mode", ["softmax", "sigmoid"])
 def test_one_training_step_of_a_router(mode):
     """norm -> route -> balance -> their gradients, chained as a training loop
