@@ -13,11 +13,11 @@
 // up the parts of dW and db.  A few tokens take one launch on the fp32 units
 // instead (few_tokens below).
 //
-// 8192 tokens x 256 experts x 4096: 74 us of device time, of which the
-// preparation 12, dW 48 (63 % of the tensor cores' cycles; every pair of blocks
-// streams all of dl's pieces beside its x, 268 MB out of L2) and dx 27, half of
-// it beside the tail of dW.  2048 x 32 x 4096: 22 us, three launches' latency
-// and x read and dx written once each.
+// 8192 tokens x 256 experts x 4096: 75 to 82 us of device time (alone and with
+// cold caches the preparation takes 12, dW 48, dx 27).  dW is bound by its
+// operands: the tensor cores are active 63 % of its time, and every tile of 256
+// h reads all of dl's pieces again, 201 of the 268 MB that cross from L2.  2048 x
+// 32 x 4096: 22 us, the latency of three launches over 35 MB.
 //
 // fp32 operands on 16-bit tensor cores.  dW needs fp32 accuracy: x is bf16
 // already, and dl is taken as the sum of three bf16 numbers (its rounding, the
