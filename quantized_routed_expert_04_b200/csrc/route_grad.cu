@@ -325,19 +325,24 @@ __device__ __forceinline__ void cluster_arrive(uint32_t bar_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_addr) : "memory");
 }
 // Loads into this block's shared memory, counted on a barrier of either block
-// of the pair (a shared::cluster address).
+// of the pair (a shared::cluster address); issued, like the MMAs, by one lane of
+// a warp that runs as a whole.
 __device__ __forceinline__ void tma2_load_2d(void *dst, const void *tmap, int c0, int c1, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(smem_u32(dst)),
       "l"(tmap), "r"(c0), "r"(c1), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void tma2_load_3d(void *dst, const void *tmap, int c0, int c1, int c2,
                                              uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(smem_u32(dst)),
       "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
 }
@@ -501,44 +506,46 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const long long units = (long long)tiles * n_kb;
   const long long u0 = run_begin(units, p.pairs, pair), u1 = run_begin(units, p.pairs, pair + 1);
   if (warp == 0) {
-    if (lane == 0) {
-      Ring r;
-      long long issued = 0;
-      bool ok = true;
-      for (long long u = u0; u < u1; ++u) {
-        if (!mbar_wait(&s.empty[r.st], r.ph ^ 1u, p.status)) { ok = false; break; }
-        const int tile = (int)(u / n_kb), t = (int)(u - (long long)tile * n_kb) * kDwTok;
-        uint8_t *a = smem + r.st * kStage, *b = a + 2 * kDwBox;
-        const uint32_t bar = cluster_addr(&s.full[r.st], 0);
-        if (rank == 0) mbar_arrive_expect_tx(&s.full[r.st], 2 * kStage - (kForm == 0 ? kDwBox : 0));
+    Ring r;
+    const int n = (int)(u1 - u0);
+    int tile = (int)(u0 / n_kb), kb = (int)(u0 - (long long)tile * n_kb), issued = 0;
+    const uint32_t bar0 = cluster_addr(&s.full[0], 0);
+    bool ok = true;
+    for (; issued < n; ++issued) {
+      if (!warp_wait(&s.empty[r.st], r.ph ^ 1u, lane, p.status)) { ok = false; break; }
+      const int t = kb * kDwTok, h = tile * kTileH + 128 * (int)rank;
+      uint8_t *a = smem + r.st * kStage, *b = a + 2 * kDwBox;
+      const uint32_t bar = bar0 + 8 * r.st;
+      if (rank == 0 && lane == 0)
+        mbar_arrive_expect_tx(&s.full[r.st], 2 * kStage - (kForm == 0 ? kDwBox : 0));
+      __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          tma2_load_2d(a + i * kDwBox, &map_x, tile * kTileH + 128 * (int)rank + 64 * i, t, bar);
-        const int rk = (int)rank;
-        auto piece = [&](int box, int c, int e) {
-          tma2_load_3d(b + box * kDwBox, &map_dl, e, t, c, bar);
-        };
-        if (kForm == 0) {
-          piece(0, 2 * rk, 0);
-          if (rk == 0) piece(1, 1, 0);
-        } else if (kForm == 1) {
-          piece(0, rk, 0);
-          piece(1, rk, 64);
-          piece(2, 2, 64 * rk);
-        } else {
+      for (int i = 0; i < 2; ++i) tma2_load_2d(a + i * kDwBox, &map_x, h + 64 * i, t, bar);
+      const int rk = (int)rank;
+      auto piece = [&](int box, int c, int e) { tma2_load_3d(b + box * kDwBox, &map_dl, e, t, c, bar); };
+      if (kForm == 0) {
+        piece(0, 2 * rk, 0);
+        if (rk == 0) piece(1, 1, 0);
+      } else if (kForm == 1) {
+        piece(0, rk, 0);
+        piece(1, rk, 64);
+        piece(2, 2, 64 * rk);
+      } else {
 #pragma unroll
-          for (int c = 0; c < 3; ++c) {
-            piece(2 * c, c, 128 * rk);
-            piece(2 * c + 1, c, 128 * rk + 64);
-          }
+        for (int c = 0; c < 3; ++c) {
+          piece(2 * c, c, 128 * rk);
+          piece(2 * c + 1, c, 128 * rk + 64);
         }
-        ++issued;
-        r.next(p.stages);
       }
-      if (!ok && rank == 0)   // let issued copies land
-        for (long long m = issued > p.stages ? issued - p.stages : 0; m < issued; ++m)
-          (void)mbar_wait(&s.full[m % p.stages], (uint32_t)(m / p.stages) & 1u, p.status);
+      if (++kb == n_kb) {
+        kb = 0;
+        ++tile;
+      }
+      r.next(p.stages);
     }
+    if (!ok && rank == 0 && lane == 0)   // let issued copies land
+      for (int m = issued > p.stages ? issued - p.stages : 0; m < issued; ++m)
+        (void)mbar_wait(&s.full[m % p.stages], (uint32_t)(m / p.stages) & 1u, p.status);
   } else if (warp == 1) {
     if (rank == 0) {
       Ring r;
@@ -755,41 +762,45 @@ __global__ void __launch_bounds__(kDxThreads, 1)
   uint8_t *ring = smem + n_kb * 2 * kDxWBox;
   uint8_t *out_smem = ring + p.stages * kDxStage;      // [epilogue warp]
   if (warp == 0) {
-    if (lane == 0) {
-      Ring r;
-      long long issued = 0;
-      int cur = -1, w_uses = 0;
-      bool ok = true;
-      for (long long i = i0; i < i1 && ok; ++i) {
-        const int h = (int)(i / t_tiles), t = (int)(i - (long long)h * t_tiles);
-        const bool fresh = h != cur;
+    Ring r;
+    long long issued = 0;
+    int h = (int)(i0 / t_tiles), t = (int)(i0 - (long long)h * t_tiles), cur = -1, w_uses = 0;
+    const uint32_t bar0 = cluster_addr(&s.full[0], 0), w_bar0 = cluster_addr(&s.w_full[0], 0);
+    bool ok = true;
+    for (long long i = i0; i < i1 && ok; ++i) {
+      const bool fresh = h != cur;
+      if (fresh) {
+        if (cur >= 0 && !warp_wait(&s.w_empty, (w_uses - 1) & 1u, lane, p.status)) { ok = false; break; }
+        cur = h;
+        ++w_uses;
+      }
+      for (int kb = 0; kb < n_kb; ++kb) {
         if (fresh) {
-          if (cur >= 0 && !mbar_wait(&s.w_empty, (w_uses - 1) & 1u, p.status)) { ok = false; break; }
-          cur = h;
-          ++w_uses;
+          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&s.w_full[kb], 4 * kDxWBox);
+          __syncwarp();
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            tma2_load_2d(w_smem + (kb * 2 + m) * kDxWBox, &map_w, h * kTileH + 128 * (int)rank + 64 * m,
+                         64 * kb, w_bar0 + 8 * kb);
         }
-        for (int kb = 0; kb < n_kb; ++kb) {
-          if (fresh) {
-            const uint32_t bar = cluster_addr(&s.w_full[kb], 0);
-            if (rank == 0) mbar_arrive_expect_tx(&s.w_full[kb], 4 * kDxWBox);
-            for (int m = 0; m < 2; ++m)
-              tma2_load_2d(w_smem + (kb * 2 + m) * kDxWBox, &map_w, h * kTileH + 128 * (int)rank + 64 * m,
-                           64 * kb, bar);
-          }
-          if (ok && !mbar_wait(&s.empty[r.st], r.ph ^ 1u, p.status)) ok = false;
-          if (!ok) continue;   // (every copy of W that a barrier expects is still issued)
-          if (rank == 0) mbar_arrive_expect_tx(&s.full[r.st], 2 * kDxStage);
-          tma2_load_2d(ring + r.st * kDxStage, &map_dl, 64 * kb, t * kDxTok + kDxTok / 2 * (int)rank,
-                       cluster_addr(&s.full[r.st], 0));
-          ++issued;
-          r.next(p.stages);
-        }
+        if (ok && !warp_wait(&s.empty[r.st], r.ph ^ 1u, lane, p.status)) ok = false;
+        if (!ok) continue;   // (every copy of W that a barrier expects is still issued)
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&s.full[r.st], 2 * kDxStage);
+        __syncwarp();
+        tma2_load_2d(ring + r.st * kDxStage, &map_dl, 64 * kb, t * kDxTok + kDxTok / 2 * (int)rank,
+                     bar0 + 8 * r.st);
+        ++issued;
+        r.next(p.stages);
       }
-      if (!ok && rank == 0) {   // let issued copies land
-        for (long long m = issued > p.stages ? issued - p.stages : 0; m < issued; ++m)
-          (void)mbar_wait(&s.full[m % p.stages], (uint32_t)(m / p.stages) & 1u, p.status);
-        for (int kb = 0; w_uses && kb < n_kb; ++kb) (void)mbar_wait(&s.w_full[kb], (w_uses - 1) & 1u, p.status);
+      if (++t == t_tiles) {
+        t = 0;
+        ++h;
       }
+    }
+    if (!ok && rank == 0 && lane == 0) {   // let issued copies land
+      for (long long m = issued > p.stages ? issued - p.stages : 0; m < issued; ++m)
+        (void)mbar_wait(&s.full[m % p.stages], (uint32_t)(m / p.stages) & 1u, p.status);
+      for (int kb = 0; w_uses && kb < n_kb; ++kb) (void)mbar_wait(&s.w_full[kb], (w_uses - 1) & 1u, p.status);
     }
   } else if (warp == 1) {
     if (rank == 0) {
