@@ -440,10 +440,11 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int la
 }
 
 // dW[e][h] = sum_t dl[t][e] x[t][h]: M = 256 rows of h, N = the experts (all of
-// them, so x is read from memory once), K = tokens in stages of 32.  The stages
-// of all h tiles in one row are cut into equal runs, one per pair of blocks; a
-// run's part of a tile goes to slot run + tile of the workspace (or straight to
-// dW if it is the whole tile), and the last kernel adds the slots in order.
+// them, so x is read from memory once), K = tokens in stages of 32 or 64.  The
+// stages of all h tiles in one row are cut into equal runs, one per pair of
+// blocks; a run's part of a tile goes to slot run + tile of the workspace (or
+// straight to dW if it is the whole tile), and the last kernel adds the slots in
+// order.
 //
 // The tensor core cuts its running sum at every MMA (2^-23 relative, always
 // towards zero): over one chain of 910 tokens, 168 MMAs, dW came out 2.7e-6 too
@@ -460,14 +461,21 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int la
 // and the epilogue adds the columns of an expert.  Whole calls over 4096 h, in
 // form 2 and in their own: 32 experts x 2048 tokens 28.6 and 22.5 us, 128 experts
 // 32.2 and 26.7, 64 experts x 8192 tokens 64.3 and 52.5.
-constexpr int kDwTok = 32;
-constexpr int kDwBox = kDwTok * 128;   // 64 columns
+//
+// A stage is 32 tokens in form 2 (7 stages of 32 KB) and 64 in the others, whose
+// MMAs take less time than issuing the copies of so small boxes: a pair with a
+// tile to itself (4096 h) takes 0.19 us per 32 tokens with 32 experts, 0.31 in
+// stages of 32; with 128 experts 0.29 and 0.32, with 256 0.505 (3 stages of 64)
+// and 0.50.
+__host__ __device__ constexpr int dw_tok(int E) { return E <= 128 ? 64 : 32; }
 template <int kForm>
 struct DwForm {
+  static constexpr int kTok = dw_tok(64 << kForm);           // tokens per stage
+  static constexpr int kBox = kTok * 128;                    // bytes of 64 columns
   static constexpr int kCols = 32 << kForm;                  // experts per epilogue warp
   static constexpr int kSums = 3 - kForm;                    // column groups to add per expert
   static constexpr int kBoxes = kForm == 0 ? 2 : 3 * kForm;  // of dl, per block and stage
-  static constexpr int kChain = kForm == 0 ? 24 : kForm == 1 ? 12 : 8;   // stages: 48 MMAs on hi
+  static constexpr int kChain = (kForm == 0 ? 768 : kForm == 1 ? 384 : 256) / kTok;   // stages: 48 MMAs on hi
 };
 
 struct DwParams {
@@ -499,8 +507,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   grid_dependency_launch();
 
   using F = DwForm<kForm>;
-  constexpr int kStage = (2 + F::kBoxes) * kDwBox;   // per block
-  const int n_kb = (p.T + kDwTok - 1) / kDwTok;
+  constexpr int kTok = F::kTok, kBox = F::kBox;
+  constexpr int kStage = (2 + F::kBoxes) * kBox;   // per block
+  const int n_kb = (p.T + kTok - 1) / kTok;
   const int tiles = (p.H + kTileH - 1) / kTileH;
   const int pair = blockIdx.x >> 1;
   const long long units = (long long)tiles * n_kb;
@@ -513,16 +522,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     bool ok = true;
     for (; issued < n; ++issued) {
       if (!warp_wait(&s.empty[r.st], r.ph ^ 1u, lane, p.status)) { ok = false; break; }
-      const int t = kb * kDwTok, h = tile * kTileH + 128 * (int)rank;
-      uint8_t *a = smem + r.st * kStage, *b = a + 2 * kDwBox;
+      const int t = kb * kTok, h = tile * kTileH + 128 * (int)rank;
+      uint8_t *a = smem + r.st * kStage, *b = a + 2 * kBox;
       const uint32_t bar = bar0 + 8 * r.st;
       if (rank == 0 && lane == 0)
-        mbar_arrive_expect_tx(&s.full[r.st], 2 * kStage - (kForm == 0 ? kDwBox : 0));
+        mbar_arrive_expect_tx(&s.full[r.st], 2 * kStage - (kForm == 0 ? kBox : 0));
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 2; ++i) tma2_load_2d(a + i * kDwBox, &map_x, h + 64 * i, t, bar);
+      for (int i = 0; i < 2; ++i) tma2_load_2d(a + i * kBox, &map_x, h + 64 * i, t, bar);
       const int rk = (int)rank;
-      auto piece = [&](int box, int c, int e) { tma2_load_3d(b + box * kDwBox, &map_dl, e, t, c, bar); };
+      auto piece = [&](int box, int c, int e) { tma2_load_3d(b + box * kBox, &map_dl, e, t, c, bar); };
       if (kForm == 0) {
         piece(0, 2 * rk, 0);
         if (rk == 0) piece(1, 1, 0);
@@ -565,16 +574,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (!warp_wait(&s.full[r.st], r.ph, lane, p.status)) { ok = false; break; }
           tc_fence_after();
           const uint32_t a = smem_u32(smem + r.st * kStage);
-          const uint64_t ad = umma_desc_mn_sw128(a, kDwBox);
-          const uint64_t bd = umma_desc_mn_sw128(a + 2 * kDwBox, kDwBox);
+          const uint64_t ad = umma_desc_mn_sw128(a, kBox);
+          const uint64_t bd = umma_desc_mn_sw128(a + 2 * kBox, kBox);
 #pragma unroll
-          for (int ks = 0; ks < kDwTok / 16; ++ks) {
+          for (int ks = 0; ks < kTok / 16; ++ks) {
             const uint64_t ak = ad + ks * (2048 >> 4), bk = bd + ks * (2048 >> 4);
             umma2_f16(d, ak, bk, idesc, ks > 0 ? 1u : more);
-            if (kForm == 1) umma2_f16(d, ak, bk + (2 * kDwBox >> 4), idesc_lo, 1u);
+            if (kForm == 1) umma2_f16(d, ak, bk + (2 * kBox >> 4), idesc_lo, 1u);
             if (kForm == 2) {
-              umma2_f16(d, ak, bk + (2 * kDwBox >> 4), idesc, 1u);
-              umma2_f16(d, ak, bk + (4 * kDwBox >> 4), idesc, 1u);
+              umma2_f16(d, ak, bk + (2 * kBox >> 4), idesc, 1u);
+              umma2_f16(d, ak, bk + (4 * kBox >> 4), idesc, 1u);
             }
           }
           more = 1u;
@@ -641,7 +650,7 @@ struct SumParams {
 // One warp: expert e's 256 h of one tile, 8 a lane.
 __device__ __forceinline__ void sum_dw(const SumParams &q, int tile, int e, int lane) {
   const RouteGradParams &p = q.g;
-  const int tiles = (p.H + kTileH - 1) / kTileH, n_kb = (p.T + kDwTok - 1) / kDwTok;
+  const int tiles = (p.H + kTileH - 1) / kTileH, n_kb = (p.T + dw_tok(p.E) - 1) / dw_tok(p.E);
   // the runs that hold units of this tile (run r starts at unit units r / pairs)
   const long long units = (long long)tiles * n_kb, first = (long long)tile * n_kb;
   const int r0 = (int)(((first + 1) * q.pairs - 1) / units);
@@ -1090,13 +1099,35 @@ int prep_blocks(int T) {
   return n < 4 * kPairs ? n : 4 * kPairs;
 }
 int h_tiles(int H) { return (H + kTileH - 1) / kTileH; }
-// Pairs of blocks for dW: all of them, as long as each gets a stage, and at the
-// most 24 to a tile: every part of a tile is written and read again (8192 tokens
-// x 256 h x 256 experts, whole call: 33.3 us with 74 parts, 30.0 with 24, 31.8
-// with 16).
-int dw_pairs(int T, int H) {
-  const long long tiles = h_tiles(H), n_kb = (T + kDwTok - 1) / kDwTok;
-  return (int)std::min<long long>(kPairs, tiles * std::min<long long>(n_kb, 24));
+// Pairs of blocks for dW.  Each tile of h takes the same number m of runs (so
+// that no run has parts of two tiles), or the stages of all tiles are cut into 74
+// runs wherever that falls.  More runs are shorter, but every part of a tile is
+// written and read again, only then can dW be added up, and pairs that dW leaves
+// free have dx to do.  The costs below, in us, follow measurements of whole calls
+// at 256 to 7168 h, 32 to 256 experts, 64 to 8192 tokens.  E.g. 4096 h x 256
+// experts: 256 tokens 17.5 us with m = 1, 22.4 with 4, 27.4 with 74 runs; 1024
+// tokens 32.5, 27.1 (m = 3: 26.9) and 31.0; 8192 tokens 147, 70.8 and 71.5.  1024
+// h x 32 experts: 1024 tokens 12.3 with m = 8, 14.4 with 18; 8192 tokens 26.5 and
+// 22.6.  7168 h x 256 experts: 8192 tokens 114 with m = 2, 112 with 74 runs.
+int dw_pairs(int T, int E, int H) {
+  const int tiles = h_tiles(H);
+  const long long n_kb = (T + dw_tok(E) - 1) / dw_tok(E);
+  const double share = E / 256.0;
+  const double tile = T / 32.0 * (0.15 + 0.35 * share);   // one pair alone
+  const double part = 0.03 + 0.10 * share;
+  const double cut = 1.9;                                  // any parts at all
+  const long long most = std::min<long long>(kPairs, tiles * n_kb);
+  // (a run with parts of two tiles writes twice: 4 us with 256 experts)
+  int best = (int)most;
+  double cost = tile * tiles / most + (tiles % most == 0 ? 0.0 : cut + part * (most + tiles) + 0.5 + 4.0 * share);
+  for (long long m = 1; m * tiles <= most; ++m) {
+    const double c = tile / m + (m > 1 ? cut + part * m * tiles : 0.0);
+    if (c < cost) {
+      cost = c;
+      best = (int)(m * tiles);
+    }
+  }
+  return best;
 }
 
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -1119,7 +1150,7 @@ Layout layout(int T, int E, int H) {
   L.db = off;
   off += up256((size_t)prep_blocks(T) * E * 4);
   L.dw = off;
-  off += up256((size_t)(dw_pairs(T, H) + h_tiles(H)) * E * kTileH * 4);
+  off += up256((size_t)(dw_pairs(T, E, H) + h_tiles(H)) * E * kTileH * 4);
   L.total = off;
   return L;
 }
@@ -1143,13 +1174,21 @@ bool encode_planes(CUtensorMap *m, CUtensorMapDataType type, const void *base, i
 
 size_t route_grad_workspace(int T, int E, int H) { return layout(T > 0 ? T : 1, E, H).total; }
 
-// One launch on the fp32 units while the products of a block stay few: it takes
-// about 5.5 us + 0.042 us per 1024 of them, the other form 11 (8 experts) to 18
-// us (256) before its products count.  E.g. 64 experts x 2048 h: 10.8 against
-// 13.7 us with 128 tokens, 17.7 against 14.2 with 256; 256 experts x 1024: 10.1
-// against 18.5 with 32, 25.9 against 19.0 with 128.  (At most 40 KB of dl, 80 of
-// x, 32 of W and 16 of parts in shared memory.)
-bool few_tokens(int T, int E, int H) { return (long long)T * ((E + 3) / 4 * 4) * small_hs(H) <= 160 * 1024; }
+// One launch on the fp32 units while it is the shorter of the two, by times, in
+// us, that follow measurements of both forms from 8 to 256 experts and 256 to
+// 16384 h: a block's products, its rows of dl, and as many rounds of blocks as
+// there are; the other form's launches, and its preparation of more experts.  E.g.
+// 2048 h: 8 experts 9.5 against 11.1 us with 320 tokens, 14.3 against 12.9 with
+// 640; 64 experts 8.6 against 10.3 with 80, 13.4 against 10.6 with 160; 128
+// experts 10.3 against 11.6 with 60, 18.7 against 12.4 with 140; 7168 h x 64
+// experts 8.8 against 9.8 with 10, 13.1 against 10.2 with 40.  (At most 76 KB of
+// dl and W, 24 of x and 16 of parts in shared memory.)
+bool few_tokens(int T, int E, int H) {
+  const int hs = small_hs(H);
+  const double rounds = std::max(1.0, H / hs / 148.0);
+  const double products = (double)T * ((E + 3) / 4 * 4) * hs / 1024;
+  return rounds * (4.6 + 0.042 * products + 0.0105 * T) < 10.1 + 0.027 * std::max(0, E - 64) + 0.0018 * T;
+}
 
 cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stream) {
   if (few_tokens(p.T, p.E, p.H)) {
@@ -1177,15 +1216,15 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
   cudaError_t e = launch_pdl(route_grad_prep_kernel, dim3(p.tok_blocks + w_blocks),
                              dim3(32 * kPrepWarps), 0, stream, p);
   const auto kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kF16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const int pairs = dw_pairs(p.T, p.H), tiles = h_tiles(p.H);
+  const int pairs = dw_pairs(p.T, p.E, p.H), tiles = h_tiles(p.H);
   if (e == cudaSuccess && p.dW) {
     CUtensorMap mx, md;
-    if (!encode_planes(&mx, kBf16, p.x, p.H, p.T, p.H, 1, kDwTok) ||
-        !encode_planes(&md, kBf16, p.dlp, p.E, p.T, p.Epad, 3, kDwTok))
+    const int form = p.E <= 64 ? 0 : p.E <= 128 ? 1 : 2, tok = dw_tok(p.E);
+    if (!encode_planes(&mx, kBf16, p.x, p.H, p.T, p.H, 1, tok) ||
+        !encode_planes(&md, kBf16, p.dlp, p.E, p.T, p.Epad, 3, tok))
       return cudaErrorInvalidValue;
-    const int form = p.E <= 64 ? 0 : p.E <= 128 ? 1 : 2;
     const int stage = (2 + (form == 0 ? DwForm<0>::kBoxes : form == 1 ? DwForm<1>::kBoxes
-                                                                      : DwForm<2>::kBoxes)) * kDwBox;
+                                                                      : DwForm<2>::kBoxes)) * tok * 128;
     DwParams d{p.T, p.H, p.E, pairs, std::min(kMaxStages, (kSmemLimit - 2048) / stage), p.dW, p.dW_part,
                p.status};
     const int smem = d.stages * stage + 1024;
@@ -1208,8 +1247,12 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
                p.dW ? 1 : 0, p.t_scale, p.status};
     const int smem = fixed + d.stages * kDxStage + 1024;
     const long long items = (long long)((p.T + kDxTok - 1) / kDxTok) * tiles;
-    // (pairs without an item of dx help with the sums: a row of 256 per warp)
-    const long long want = std::max<long long>(items, (q.dw_rows + 2 * kSumWarps - 1) / (2 * kSumWarps));
+    // (pairs without an item of dx help with the sums, a row of 256 or an expert
+    // per warp; not many more than dW leaves room for, since those start late: 1024
+    // tokens x 256 h x 256 experts 19.7 us with 64 pairs, 16.8 with 37)
+    const int sums = q.dw_rows + (p.db ? p.E : 0);
+    const int help = std::min((sums + 2 * kSumWarps - 1) / (2 * kSumWarps), std::max(kPairs - pairs, kPairs / 2));
+    const long long want = std::max<long long>(items, help);
     e = cudaFuncSetAttribute(route_grad_dx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
       e = launch_pdl_cluster(route_grad_dx_kernel, dim3(2 * (unsigned)std::min<long long>(want, kPairs)),

@@ -403,6 +403,26 @@ def test_route_backward(T, H, E, k, mode):
     layer.close()
 
 
+# beside the borders between the forms: one launch or three; of the three, a run
+# for each tile of h, several, or runs that cut tiles anywhere
+@pytest.mark.parametrize("T,H,E,k", [
+    (60, 256, 256, 8), (61, 256, 256, 8), (77, 1024, 128, 6), (78, 1024, 128, 6), (394, 256, 8, 3),
+    (395, 256, 8, 3), (485, 128, 3, 1), (486, 128, 3, 1), (59, 4096, 64, 6), (60, 4096, 64, 6),
+    (22, 7168, 64, 4), (23, 7168, 64, 4), (1, 16384, 16, 2), (65, 16384, 250, 4), (3, 18944, 40, 2),
+    (600, 19200, 70, 3), (511, 2048, 256, 8), (1023, 4096, 128, 8), (2049, 640, 200, 8),
+    (64, 384, 256, 1), (8190, 896, 50, 2)])
+def test_route_backward_beside_the_forms_borders(T, H, E, k):
+    W, x = router(E, H, 171), acts(T, H, 172)
+    layer = make_layer(E, k, "softmax", H, W)
+    logits, idx = routing(T, E, k, 173)
+    dw = torch.randn(T, k, device="cuda", generator=gen(174))
+    dlg = torch.randn(T, E, device="cuda", generator=gen(175)) * 0.05
+    full = check_route_backward(layer, x, W, logits, idx, dw, dlg, "softmax")
+    for n in full:
+        assert torch.equal(run_route_backward(layer, x, logits, idx, dw, dlg, (n,))[n], full[n]), n
+    layer.close()
+
+
 def test_route_backward_ranges_of_values():
     # gradients of every size (1e-12 .. 1e3 in one batch) keep their relative accuracy
     T, H, E, k = 200, 256, 64, 4
