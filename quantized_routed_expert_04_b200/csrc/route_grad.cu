@@ -73,27 +73,28 @@ __device__ __forceinline__ float group_max(float v, int lanes) {
   return v;
 }
 
-// A token's inputs: lane j < k its selection j, every lane 8 logits' gradients.
+// A token's inputs, over the lanes of its group: lane j < k its selection j, lane j
+// the gradients of logits 8 j ..
 struct TokenIn {
   int id;
   float dw, l;
   float dl[8];
 };
 // Everything but the selected logit (whose place the id gives).
-__device__ __forceinline__ void load_token(const RouteGradParams &p, long long t, int lane, bool vec,
+__device__ __forceinline__ void load_token(const RouteGradParams &p, long long t, int j, bool vec,
                                            TokenIn &in) {
   in.id = -1;
   in.dw = in.l = 0.0f;
-  if (p.dw && t < p.T && lane < p.k) {
-    in.id = p.idx[t * p.k + lane];
-    in.dw = p.dw[t * p.k + lane];
+  if (p.dw && t < p.T && j < p.k) {
+    in.id = p.idx[t * p.k + j];
+    in.dw = p.dw[t * p.k + j];
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) in.dl[i] = 0.0f;
   if (!p.dlogits || t >= p.T) return;
-  const float *row = p.dlogits + t * p.E + 8 * lane;
+  const float *row = p.dlogits + t * p.E + 8 * j;
   if (vec) {
-    if (8 * lane < p.E) {
+    if (8 * j < p.E) {
       const float4 a = reinterpret_cast<const float4 *>(row)[0];
       const float4 b = reinterpret_cast<const float4 *>(row)[1];
       in.dl[0] = a.x; in.dl[1] = a.y; in.dl[2] = a.z; in.dl[3] = a.w;
@@ -102,16 +103,17 @@ __device__ __forceinline__ void load_token(const RouteGradParams &p, long long t
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (8 * lane + i < p.E) in.dl[i] = row[i];
+      if (8 * j + i < p.E) in.dl[i] = row[i];
   }
 }
 // The selected logits; a token with an id out of range (the forward writes it a
-// zero row, so dw has no meaning) loses its selections.
-__device__ __forceinline__ void load_selected(const RouteGradParams &p, long long t, int lane, TokenIn &in) {
+// zero row, so dw has no meaning) loses its selections.  group: its lanes.
+__device__ __forceinline__ void load_selected(const RouteGradParams &p, long long t, int j, unsigned group,
+                                              TokenIn &in) {
   if (!p.dw) return;
-  const bool sel = t < p.T && lane < p.k;
+  const bool sel = t < p.T && j < p.k;
   const bool bad = sel && (in.id < 0 || in.id >= p.E);
-  const bool any_bad = __any_sync(0xffffffffu, bad);
+  const unsigned any_bad = __ballot_sync(0xffffffffu, bad) & group;
   if (bad) set_status(p.status, STATUS_BAD_ROUTING);
   if (any_bad) in.id = -1;
   if (sel && in.id >= 0) in.l = p.logits[t * p.E + in.id];
@@ -150,12 +152,16 @@ __device__ __forceinline__ uint4 pack_f16(const float v[8], float mul) {
 }
 constexpr float kWScale = 256.0f;
 
-// Blocks 0 .. tok_blocks - 1: rows of dl, one warp per token at a time, each
-// lane 8 consecutive experts, as three bf16 pieces and as scaled f16, and the
-// block's share of db.  The blocks behind them: W as f16.
+// Blocks 0 .. tok_blocks - 1: rows of dl, a group of kG lanes per token, each lane
+// 8 consecutive experts, as three bf16 pieces and as scaled f16, and the block's
+// share of db.  The blocks behind them: W as f16.  (kG holds the experts and the
+// selections; a warp per token whatever their number made the whole call over
+// 8192 tokens x 32 experts x 4096 take 44 us, 41 with 8 lanes each.)
+template <int kG>
 __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const RouteGradParams p) {
-  // a row per warp: the scattered selections, at the end the sums for db
-  __shared__ __align__(16) float s_row[kPrepWarps][kMaxExperts];
+  constexpr int kTok = 32 / kG;   // tokens a warp works on at once
+  // a row per group: the scattered selections, at the end the sums for db
+  __shared__ __align__(16) float s_row[kPrepWarps * kTok][8 * kG];
   for (int i = threadIdx.x; i < kPrepWarps * kMaxExperts; i += blockDim.x) (&s_row[0][0])[i] = 0.0f;
   __syncthreads();
   grid_dependency_wait();
@@ -176,32 +182,33 @@ __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const 
     if (over) set_status(p.status, STATUS_RANGE);
     return;
   }
+  const int j = lane % kG, base = lane - j;   // the group's lanes: base ..
+  const unsigned group = (kG == 32 ? 0xffffffffu : (1u << (kG & 31)) - 1u) << base;
+  float *row = s_row[warp * kTok + lane / kG];
   const bool vec = E % 8 == 0 && (reinterpret_cast<uintptr_t>(p.dlogits) & 15) == 0;
   float db[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) db[i] = 0.0f;
-  auto finish = [&](long long t, TokenIn &in) {
-    if (t >= p.T) return;
+  auto finish = [&](long long t, TokenIn &in) {   // (all lanes of the warp, past the last token too)
     float (&v)[8] = in.dl;
     if (p.dw) {
       // scattered through a row of shared memory that is zero in between; of
       // lanes with the same expert the first adds up all, in lane order
-      float g = weight_grad(p.mode, in.id, in.l, in.dw, 32);
-      const unsigned same = __match_any_sync(0xffffffffu, in.id);
+      float g = weight_grad(p.mode, in.id, in.l, in.dw, kG);
+      const unsigned same = __match_any_sync(0xffffffffu, in.id) & group;
       const bool first = (same & ((1u << lane) - 1u)) == 0u && in.id >= 0;
       if (__any_sync(0xffffffffu, in.id >= 0 && (same & (same - 1u)) != 0u)) {
         float sum = 0.0f;
-        for (int j = 0; j < p.k; ++j) {
-          const float gj = __shfl_sync(0xffffffffu, g, j);
-          if ((same >> j) & 1u) sum += gj;
+        for (int q = 0; q < p.k; ++q) {
+          const float gq = __shfl_sync(0xffffffffu, g, base + q);
+          if ((same >> (base + q)) & 1u) sum += gq;
         }
         g = sum;
       }
-      float *row = s_row[warp];
       if (first) row[in.id] = g;
       __syncwarp();
-      const float4 a = reinterpret_cast<const float4 *>(row)[2 * lane];
-      const float4 b = reinterpret_cast<const float4 *>(row)[2 * lane + 1];
+      const float4 a = reinterpret_cast<const float4 *>(row)[2 * j];
+      const float4 b = reinterpret_cast<const float4 *>(row)[2 * j + 1];
       v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
       v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
       __syncwarp();
@@ -209,19 +216,21 @@ __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const 
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) db[i] += v[i];
-    const size_t at = (size_t)t * (p.Epad / 8) + lane;
+    const size_t at = (size_t)t * (p.Epad / 8) + j;
+    const bool out_here = t < p.T && 8 * j < E;
     if (p.dl16) {
       // the power of two below the row's largest magnitude (within 2^-126 .. 2^126)
       float m = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
-      m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+      m = group_max(m, kG);
       const int ex = m == 0.0f ? 0 : min(max((int)(__float_as_uint(m) >> 23) - 127, -126), 126);
-      if (8 * lane < E)
+      if (out_here)
         reinterpret_cast<uint4 *>(p.dl16)[at] = pack_f16(v, __uint_as_float((uint32_t)(127 - ex) << 23));
-      if (lane == 0) p.t_scale[t] = __uint_as_float((uint32_t)(127 + ex) << 23) * (1.0f / kWScale);
+      if (t < p.T && j == 0)
+        p.t_scale[t] = __uint_as_float((uint32_t)(127 + ex) << 23) * (1.0f / kWScale);
     }
-    if (p.dlp && 8 * lane < E) {
+    if (p.dlp && out_here) {
       const size_t plane = (size_t)p.T * p.Epad / 8;
       uint4 *out = reinterpret_cast<uint4 *>(p.dlp) + at;
       out[0] = take_bf16(v);
@@ -230,24 +239,25 @@ __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const 
     }
   };
   // two tokens a turn: their loads are in flight together
-  const long long step = (long long)p.tok_blocks * kPrepWarps;
-  for (long long t = (long long)blockIdx.x * kPrepWarps + warp; t < p.T; t += 2 * step) {
+  const long long step = (long long)p.tok_blocks * kPrepWarps * kTok;
+  for (long long t0 = ((long long)blockIdx.x * kPrepWarps + warp) * kTok; t0 < p.T; t0 += 2 * step) {
+    const long long t = t0 + lane / kG;
     TokenIn a, b;
-    load_token(p, t, lane, vec, a);
-    load_token(p, t + step, lane, vec, b);
-    load_selected(p, t, lane, a);
-    load_selected(p, t + step, lane, b);
+    load_token(p, t, j, vec, a);
+    load_token(p, t + step, j, vec, b);
+    load_selected(p, t, j, group, a);
+    load_selected(p, t + step, j, group, b);
     finish(t, a);
-    finish(t + step, b);
+    if (t0 + step < p.T) finish(t + step, b);
   }
   if (p.db_part) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_row[warp][8 * lane + i] = db[i];
+    for (int i = 0; i < 8; ++i) row[8 * j + i] = db[i];
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
       float s = s_row[0][e];
 #pragma unroll
-      for (int w = 1; w < kPrepWarps; ++w) s += s_row[w][e];
+      for (int w = 1; w < kPrepWarps * kTok; ++w) s += s_row[w][e];
       p.db_part[(size_t)blockIdx.x * E + e] = s;
     }
   }
@@ -1094,8 +1104,16 @@ __global__ void __launch_bounds__(kSmallThreads) route_grad_small_kernel(const R
 constexpr int kPairs = 74;   // 148 multiprocessors
 static_assert(4 * kPairs <= 320, "sum_db reads up to 320 blocks' parts");
 
-int prep_blocks(int T) {
-  const int n = (T + kPrepWarps - 1) / kPrepWarps;
+// Lanes of the preparation per token: the power of two that holds the experts, 8 a
+// lane, and the selections.
+int prep_lanes(int E, int k) {
+  int g = 8;
+  while (8 * g < E || g < k) g *= 2;
+  return g;
+}
+// (the selections of 32 lanes at the most: what the workspace's size goes by)
+int prep_blocks(int T, int lanes) {
+  const int per = kPrepWarps * 32 / lanes, n = (T + per - 1) / per;
   return n < 4 * kPairs ? n : 4 * kPairs;
 }
 int h_tiles(int H) { return (H + kTileH - 1) / kTileH; }
@@ -1148,7 +1166,7 @@ Layout layout(int T, int E, int H) {
   L.w16 = off;
   off += up256((size_t)E * H * 2);
   L.db = off;
-  off += up256((size_t)prep_blocks(T) * E * 4);
+  off += up256((size_t)prep_blocks(T, 32) * E * 4);
   L.dw = off;
   off += up256((size_t)(dw_pairs(T, E, H) + h_tiles(H)) * E * kTileH * 4);
   L.total = off;
@@ -1203,7 +1221,8 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
   const Layout L = layout(p.T, p.E, p.H);
   char *w = static_cast<char *>(workspace);
   p.Epad = (p.E + 7) / 8 * 8;
-  p.tok_blocks = prep_blocks(p.T);
+  const int lanes = prep_lanes(p.E, p.k);
+  p.tok_blocks = prep_blocks(p.T, lanes);
   p.dlp = p.dW ? reinterpret_cast<__nv_bfloat16 *>(w + L.dlp) : nullptr;
   p.dl16 = p.dx ? reinterpret_cast<__half *>(w + L.dl16) : nullptr;
   p.t_scale = reinterpret_cast<float *>(w + L.t_scale);
@@ -1213,8 +1232,10 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
   const size_t n8 = (size_t)p.E * p.H / 8;
   const int w_blocks =
       p.dx ? (int)std::min<size_t>((n8 + 32 * kPrepWarps - 1) / (32 * kPrepWarps), 4 * kPairs) : 0;
-  cudaError_t e = launch_pdl(route_grad_prep_kernel, dim3(p.tok_blocks + w_blocks),
-                             dim3(32 * kPrepWarps), 0, stream, p);
+  cudaError_t e = launch_pdl(lanes == 8    ? route_grad_prep_kernel<8>
+                             : lanes == 16 ? route_grad_prep_kernel<16>
+                                           : route_grad_prep_kernel<32>,
+                             dim3(p.tok_blocks + w_blocks), dim3(32 * kPrepWarps), 0, stream, p);
   const auto kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kF16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const int pairs = dw_pairs(p.T, p.E, p.H), tiles = h_tiles(p.H);
   if (e == cudaSuccess && p.dW) {
