@@ -13,11 +13,12 @@
 // up the parts of dW and db.  A few tokens take one launch on the fp32 units
 // instead (few_tokens below).
 //
-// 8192 tokens x 256 experts x 4096: 75 to 82 us of device time (alone and with
-// cold caches the preparation takes 12, dW 48, dx 27).  dW is bound by its
-// operands: the tensor cores are active 63 % of its time, and every tile of 256
-// h reads all of dl's pieces again, 201 of the 268 MB that cross from L2.  2048 x
-// 32 x 4096: 22 us, the latency of three launches over 35 MB.
+// 8192 tokens x 256 experts x 4096: 70 us of device time (alone and with cold
+// caches the preparation takes 12, dW 44, dx 28).  dW is bound by the tensor
+// cores, active for 87 % of the time on the multiprocessors that it uses (51.5
+// GFLOP for the three pieces, 33 us without the preparation and the sums); dx by
+// writing 67 MB.  2048 x 32 x 4096: 20 us, the latency of three launches over 35
+// MB.
 //
 // fp32 operands on 16-bit tensor cores.  dW needs fp32 accuracy: x is bf16
 // already, and dl is taken as the sum of three bf16 numbers (its rounding, the
@@ -156,7 +157,7 @@ constexpr float kWScale = 256.0f;
 // 8 consecutive experts, as three bf16 pieces and as scaled f16, and the block's
 // share of db.  The blocks behind them: W as f16.  (kG holds the experts and the
 // selections; a warp per token whatever their number made the whole call over
-// 8192 tokens x 32 experts x 4096 take 44 us, 41 with 8 lanes each.)
+// 8192 tokens x 32 experts x 4096 take 44.1 us, 42.2 with 8 lanes each.)
 template <int kG>
 __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const RouteGradParams p) {
   constexpr int kTok = 32 / kG;   // tokens a warp works on at once
@@ -469,8 +470,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int la
 //   form 1, up to 128 experts:  two: hi 128 | mid 128, then lo 128 on top of hi
 //   form 2, up to 256 experts:  three: hi, mid, lo, 256 columns each
 // and the epilogue adds the columns of an expert.  Whole calls over 4096 h, in
-// form 2 and in their own: 32 experts x 2048 tokens 28.6 and 22.5 us, 128 experts
-// 32.2 and 26.7, 64 experts x 8192 tokens 64.3 and 52.5.
+// form 2 and in their own: 32 experts x 2048 tokens 26.5 and 19.9 us, 128 experts
+// 29.0 and 23.2, 64 experts x 8192 tokens 59.4 and 43.2.
 //
 // A stage is 32 tokens in form 2 (7 stages of 32 KB) and 64 in the others, whose
 // MMAs take less time than issuing the copies of so small boxes: a pair with a
@@ -765,8 +766,8 @@ __global__ void __launch_bounds__(kDxThreads, 1)
   // dx needs what the preparation wrote, and the dW kernel lets this grid start
   // only once all its blocks have seen the preparation complete: only the warps
   // that add up dW's parts wait for the dW kernel itself, so that dx runs beside
-  // it wherever multiprocessors are free (8192 tokens x 256 experts x 4096: 74.4
-  // us, 78.9 with every warp waiting).
+  // it wherever multiprocessors are free (128 tokens x 64 experts x 2048: 10.5 us,
+  // 13.4 with every warp waiting; 8192 x 256 x 4096: 70.9 and 71.7).
   if (!p.after_dw || warp >= 2 + kDxEpiWarps) {
     grid_dependency_wait();
     grid_dependency_launch();
@@ -910,9 +911,8 @@ __global__ void __launch_bounds__(kDxThreads, 1)
 // ---------------------------------------------------------------- few tokens
 // The whole of it in one launch on the fp32 units: a block per 16 or 32 h
 // computes dl (every block the same) into shared memory and takes its columns of
-// dW and dx.  The three launches of the other form take 11 to 18 us however small
-// the batch is; this one takes 5 us with one token, 10.8 with 128 tokens x 64
-// experts x 2048 (13.7).
+// dW and dx.  The three launches of the other form take 9 to 15 us however small
+// the batch is; this one takes 5 us with one token.
 constexpr int kSmallThreads = 1024;
 
 __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
