@@ -386,7 +386,7 @@ struct NormGradParams {
 // filled by bulk copies, so that several rows of all three inputs are in flight
 // while one is reduced: on 8192 rows of 4096 bf16 with a direct gradient, plain
 // loads with one row ahead in registers took 98 us (waiting for loads; and 88
-// through the ring with elements converted one by one), now 47 us.  The barrier
+// through the ring with elements converted one by one), now 44 us.  The barrier
 // of the row's reduction also frees its stage: every thread has its elements in
 // registers by then.  A copy that does not arrive within the limit of its wait
 // ends the copies; its row and all the thread's rows behind it become NaN, and

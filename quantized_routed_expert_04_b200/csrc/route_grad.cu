@@ -13,7 +13,7 @@
 // up the parts of dW and db.  A few tokens take one launch on the fp32 units
 // instead (few_tokens below).
 //
-// 8192 tokens x 256 experts x 4096: 70 us of device time (alone and with cold
+// 8192 tokens x 256 experts x 4096: 70 to 80 us of device time (alone and with cold
 // caches the preparation takes 12, dW 44, dx 28).  dW is bound by the tensor
 // cores, active for 87 % of the time on the multiprocessors that it uses (51.5
 // GFLOP for the three pieces, 33 us without the preparation and the sums); dx by
