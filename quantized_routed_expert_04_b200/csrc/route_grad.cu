@@ -709,20 +709,25 @@ __device__ __forceinline__ void sum_db(const RouteGradParams &p, int e, int lane
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (lane == 0) p.db[e] = (float)s;
 }
-// The whole of it, by warp `warp` of `warps`.
-__device__ __forceinline__ void sum_parts(const SumParams &q, int warp, int warps, int lane) {
-  if (q.g.db)
-    for (int e = warp; e < q.g.E; e += warps) sum_db(q.g, e, lane);
-  for (int i = warp; i < q.dw_rows; i += warps) {
-    const int tile = i / q.g.E;
-    sum_dw(q, tile, i - tile * q.g.E, lane);
+// Rows of all this: db's experts, then dW's rows of 256 h.
+__host__ __device__ inline int sum_rows(const SumParams &q) { return (q.g.db ? q.g.E : 0) + q.dw_rows; }
+// Rows [begin, end), by warp `warp` of `warps`.
+__device__ __forceinline__ void sum_parts(const SumParams &q, int begin, int end, int warp, int warps, int lane) {
+  const int n_db = q.g.db ? q.g.E : 0;
+  for (int r = begin + warp; r < end; r += warps) {
+    if (r < n_db) {
+      sum_db(q.g, r, lane);
+    } else {
+      const int i = r - n_db, tile = i / q.g.E;
+      sum_dw(q, tile, i - tile * q.g.E, lane);
+    }
   }
 }
 // ... in a launch of its own, where dx is not wanted.
 __global__ void __launch_bounds__(256) route_grad_sum_kernel(const SumParams q) {
   grid_dependency_wait();
   grid_dependency_launch();
-  sum_parts(q, blockIdx.x * 8 + (threadIdx.x >> 5), gridDim.x * 8, threadIdx.x & 31);
+  sum_parts(q, 0, sum_rows(q), blockIdx.x * 8 + (threadIdx.x >> 5), gridDim.x * 8, threadIdx.x & 31);
 }
 
 // dx[t][h] = sum_e dl[t][e] W[e][h]: M = 256 tokens, N = 256 rows of h, K = the
@@ -743,6 +748,7 @@ constexpr int kDxThreads = 32 * (2 + kDxEpiWarps + kSumWarps);
 struct DxParams {
   int T, H, E, stages;
   int after_dw;           // the kernel before this one on the stream is dW's
+  int spare_rows;         // rows of the sums that the spare warps take
   const float *t_scale;   // [T]
   int *status;
 };
@@ -902,8 +908,13 @@ __global__ void __launch_bounds__(kDxThreads, 1)
       if (lane == 0 && h0 < p.H && tok0 < p.T) tma_store_2d(&map_dx, tile, h0, tok0);
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
+    if (p.spare_rows < sum_rows(q)) {
+      grid_dependency_wait();
+      sum_parts(q, p.spare_rows, sum_rows(q), blockIdx.x * kDxEpiWarps + warp - 2, gridDim.x * kDxEpiWarps, lane);
+    }
   } else {
-    sum_parts(q, blockIdx.x * kSumWarps + warp - 2 - kDxEpiWarps, gridDim.x * kSumWarps, lane);
+    sum_parts(q, 0, p.spare_rows, blockIdx.x * kSumWarps + warp - 2 - kDxEpiWarps, gridDim.x * kSumWarps, lane);
   }
   pair_end(s, warp);
 }
@@ -1265,21 +1276,23 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
       return cudaErrorInvalidValue;
     const int fixed = (p.E + 63) / 64 * 2 * kDxWBox + kDxEpiWarps * kDxOut;
     DxParams d{p.T, p.H, p.E, std::min(kMaxStages, (kSmemLimit - 2048 - fixed) / kDxStage),
-               p.dW ? 1 : 0, p.t_scale, p.status};
+               p.dW ? 1 : 0, 0, p.t_scale, p.status};
     const int smem = fixed + d.stages * kDxStage + 1024;
     const long long items = (long long)((p.T + kDxTok - 1) / kDxTok) * tiles;
     // (pairs without an item of dx help with the sums, a row of 256 or an expert
     // per warp; not many more than dW leaves room for, since those start late: 1024
     // tokens x 256 h x 256 experts 19.7 us with 64 pairs, 16.8 with 37)
-    const int sums = q.dw_rows + (p.db ? p.E : 0);
+    const int sums = sum_rows(q);
     const int help = std::min((sums + 2 * kSumWarps - 1) / (2 * kSumWarps), std::max(kPairs - pairs, kPairs / 2));
-    const long long want = std::max<long long>(items, help);
+    const int grid = (int)std::min<long long>(std::max<long long>(items, help), kPairs);
+    // a row takes a spare warp about 1.2 us and an item of dx its pair 2.5: what the
+    // spare warps would not have done by the end of dx, the epilogue's do then
+    d.spare_rows = (int)std::min<long long>(sums, 2LL * grid * kSumWarps * (1 + 2 * (items / grid)));
     e = cudaFuncSetAttribute(route_grad_dx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
-      e = launch_pdl_cluster(route_grad_dx_kernel, dim3(2 * (unsigned)std::min<long long>(want, kPairs)),
-                             2, dim3(kDxThreads), smem, stream, d, q, md, mw, mo);
-  } else if (e == cudaSuccess && (p.db || q.dw_rows)) {
-    const int blocks = (std::max(p.E, q.dw_rows) + 7) / 8;
+      e = launch_pdl_cluster(route_grad_dx_kernel, dim3(2 * grid), 2, dim3(kDxThreads), smem, stream, d, q, md, mw, mo);
+  } else if (e == cudaSuccess && sum_rows(q)) {
+    const int blocks = (sum_rows(q) + 7) / 8;
     e = launch_pdl(route_grad_sum_kernel, dim3(blocks), dim3(256), 0, stream, q);
   }
   return e;
