@@ -9,8 +9,8 @@
 //   dW = dl^T x,   db = sum_t dl,   dx = dl W.
 //
 // Three launches: the operands in 16 bits; dW on the tensor cores (tcgen05,
-// accumulators in tensor memory); dx on the tensor cores, whose spare warps add
-// up the parts of dW and db.  A few tokens take one launch on the fp32 units
+// accumulators in tensor memory); dx on the tensor cores, whose spare warps, and
+// after dx the others, add up the parts of dW and db.  A few tokens take one launch on the fp32 units
 // instead (few_tokens below).
 //
 // 8192 tokens x 256 experts x 4096: 70 to 80 us of device time (alone and with cold
@@ -1134,10 +1134,11 @@ int h_tiles(int H) { return (H + kTileH - 1) / kTileH; }
 // written and read again, only then can dW be added up, and pairs that dW leaves
 // free have dx to do.  The costs below, in us, follow measurements of whole calls
 // at 256 to 7168 h, 32 to 256 experts, 64 to 8192 tokens.  E.g. 4096 h x 256
-// experts: 256 tokens 17.5 us with m = 1, 22.4 with 4, 27.4 with 74 runs; 1024
-// tokens 32.5, 27.1 (m = 3: 26.9) and 31.0; 8192 tokens 147, 70.8 and 71.5.  1024
-// h x 32 experts: 1024 tokens 12.3 with m = 8, 14.4 with 18; 8192 tokens 26.5 and
-// 22.6.  7168 h x 256 experts: 8192 tokens 114 with m = 2, 112 with 74 runs.
+// experts: 256 tokens 17.0 us with m = 1, 24.1 with 4, 24.9 with 74 runs; 1024
+// tokens 32.5, 26.3 (m = 3, which is taken: 26.0) and 28.2; 8192 tokens 147, 71.4
+// and 72.4.  1024 h x 32 experts: 1024 tokens 11.3 with m = 8, 14.1 with 18; 8192
+// tokens 21.1 and 19.8.  7168 h x 256 experts: 8192 tokens 114.6 with m = 2, 112.2
+// with 74 runs.
 int dw_pairs(int T, int E, int H) {
   const int tiles = h_tiles(H);
   const long long n_kb = (T + dw_tok(E) - 1) / dw_tok(E);
@@ -1281,12 +1282,13 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
     const long long items = (long long)((p.T + kDxTok - 1) / kDxTok) * tiles;
     // (pairs without an item of dx help with the sums, a row of 256 or an expert
     // per warp; not many more than dW leaves room for, since those start late: 1024
-    // tokens x 256 h x 256 experts 19.7 us with 64 pairs, 16.8 with 37)
+    // tokens x 256 h x 256 experts 19.7 us with 64 pairs, 16.7 with 37)
     const int sums = sum_rows(q);
     const int help = std::min((sums + 2 * kSumWarps - 1) / (2 * kSumWarps), std::max(kPairs - pairs, kPairs / 2));
     const int grid = (int)std::min<long long>(std::max<long long>(items, help), kPairs);
     // a row takes a spare warp about 1.2 us and an item of dx its pair 2.5: what the
-    // spare warps would not have done by the end of dx, the epilogue's do then
+    // spare warps would not have done by the end of dx, the epilogue's do then (2048
+    // tokens x 1024 h x 256 experts: 20.0 us, 22.6 with the spare warps alone)
     d.spare_rows = (int)std::min<long long>(sums, 2LL * grid * kSumWarps * (1 + 2 * (items / grid)));
     e = cudaFuncSetAttribute(route_grad_dx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
