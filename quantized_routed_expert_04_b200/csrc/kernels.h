@@ -158,9 +158,10 @@ struct RouteGradParams {
   int Epad, tok_blocks;
   int small_red;           // few tokens: offset of dW's parts in shared memory
   __nv_bfloat16 *dlp;      // [3][T][Epad] bf16 pieces of dl
-  __half *dl16;            // [T][Epad] dl / t_scale (up to the scale of W16)
+  __half *dl16;            // [T][Epad] dl / t_scale
   float *t_scale;          // [T]
-  __half *W16;             // [E][H] W, scaled
+  __half *W16;             // [E][H] W / w_scale
+  float *w_scale;          // [H / 32], one for 32 columns
   float *db_part;          // [tok_blocks][E]
   float *dW_part;          // parts of dW, [slot][E][256]
 };

@@ -24,9 +24,11 @@
 // already, and dl is taken as the sum of three bf16 numbers (its rounding, the
 // rounding of what is left, and again: 24 bits): three exact products per
 // element, added in fp32.  dx is rounded to bf16 (8 bits) at the end: dl and W
-// are rounded once to f16 (11 bits), dl divided by a power of two per token
-// that puts its row's largest magnitude in [1, 2), W times 2^8.  That is a third
-// of the products that two bf16 pieces of each would take.
+// are rounded once to f16 (11 bits), each row of dl and each 32 columns of W
+// times the power of two that puts their largest magnitude in [2^14, 2^15), the
+// top of f16's range: whatever the sizes of the weights, what is lost below f16's
+// normal range is 2^-39 of the largest.  That is a third of the products that two
+// bf16 pieces of each would take.
 
 #include <cuda.h>
 
@@ -151,11 +153,23 @@ __device__ __forceinline__ uint4 pack_f16(const float v[8], float mul) {
                     h2_bits(__floats2half2_rn(v[4] * mul, v[5] * mul)),
                     h2_bits(__floats2half2_rn(v[6] * mul, v[7] * mul)));
 }
-constexpr float kWScale = 256.0f;
+// What takes a largest magnitude m to [2^14, 2^15), and back (m below 2^-112: as
+// far as a power of two goes, 2^126).
+struct F16Scale {
+  float mul, back;
+};
+__device__ __forceinline__ F16Scale f16_scale(float m) {
+  const int ex = min(max((int)(__float_as_uint(m) >> 23) - 127, -112), 127);
+  return {__uint_as_float((uint32_t)(127 + 14 - ex) << 23), __uint_as_float((uint32_t)(127 - 14 + ex) << 23)};
+}
+constexpr int kWCols = 32;             // columns of W that share a scale
+// Router weights from here on are reported (STATUS_RANGE) where dx is wanted.
+constexpr float kWLimit = kF16Overflow / 256.0f;
 
 // Blocks 0 .. tok_blocks - 1: rows of dl, a group of kG lanes per token, each lane
 // 8 consecutive experts, as three bf16 pieces and as scaled f16, and the block's
-// share of db.  The blocks behind them: W as f16.  (kG holds the experts and the
+// share of db.  The blocks behind them: 32 columns of W as scaled f16, all experts
+// in registers between the search for the largest and the rounding.  (kG holds the experts and the
 // selections; a warp per token whatever their number made the whole call over
 // 8192 tokens x 32 experts x 4096 take 44.1 us, 42.2 with 8 lanes each.)
 template <int kG>
@@ -169,17 +183,32 @@ __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const 
   grid_dependency_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = p.E;
   if ((int)blockIdx.x >= p.tok_blocks) {
-    const size_t n8 = (size_t)E * p.H / 8;
-    const size_t step = (size_t)(gridDim.x - p.tok_blocks) * blockDim.x;
-    bool over = false;
-    for (size_t i = (size_t)(blockIdx.x - p.tok_blocks) * blockDim.x + threadIdx.x; i < n8; i += step) {
-      const float4 a = reinterpret_cast<const float4 *>(p.W)[2 * i];
-      const float4 b = reinterpret_cast<const float4 *>(p.W)[2 * i + 1];
-      const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    constexpr int kRows = 32 * kPrepWarps / (kWCols / 4);   // experts at once
+    constexpr int kTurns = kMaxExperts / kRows;
+    const int tile = (int)blockIdx.x - p.tok_blocks, e0 = threadIdx.x / (kWCols / 4);
+    const size_t at = (size_t)e0 * p.H + kWCols * tile + 4 * (threadIdx.x % (kWCols / 4));
+    float4 v[kTurns];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) over |= fabsf(v[k]) * kWScale >= kF16Overflow;
-      reinterpret_cast<uint4 *>(p.W16)[i] = pack_f16(v, kWScale);
-    }
+    for (int k = 0; k < kTurns; ++k)
+      v[k] = e0 + k * kRows < E ? *reinterpret_cast<const float4 *>(p.W + at + (size_t)k * kRows * p.H)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k)
+      m = fmaxf(m, fmaxf(fmaxf(fabsf(v[k].x), fabsf(v[k].y)), fmaxf(fabsf(v[k].z), fabsf(v[k].w))));
+    const bool over = m >= kWLimit;
+    m = group_max(m, 32);
+    float *most = &s_row[0][0];
+    if (lane == 0) most[warp] = m;
+    __syncthreads();
+    const F16Scale scale = f16_scale(group_max(most[lane % kPrepWarps], kPrepWarps));
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k)
+      if (e0 + k * kRows < E)
+        *reinterpret_cast<uint2 *>(p.W16 + at + (size_t)k * kRows * p.H) =
+            make_uint2(h2_bits(__floats2half2_rn(v[k].x * scale.mul, v[k].y * scale.mul)),
+                       h2_bits(__floats2half2_rn(v[k].z * scale.mul, v[k].w * scale.mul)));
+    if (threadIdx.x == 0) p.w_scale[tile] = scale.back;
     if (over) set_status(p.status, STATUS_RANGE);
     return;
   }
@@ -220,16 +249,13 @@ __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const 
     const size_t at = (size_t)t * (p.Epad / 8) + j;
     const bool out_here = t < p.T && 8 * j < E;
     if (p.dl16) {
-      // the power of two below the row's largest magnitude (within 2^-126 .. 2^126)
       float m = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
       m = group_max(m, kG);
-      const int ex = m == 0.0f ? 0 : min(max((int)(__float_as_uint(m) >> 23) - 127, -126), 126);
-      if (out_here)
-        reinterpret_cast<uint4 *>(p.dl16)[at] = pack_f16(v, __uint_as_float((uint32_t)(127 - ex) << 23));
-      if (t < p.T && j == 0)
-        p.t_scale[t] = __uint_as_float((uint32_t)(127 + ex) << 23) * (1.0f / kWScale);
+      const F16Scale scale = f16_scale(m);
+      if (out_here) reinterpret_cast<uint4 *>(p.dl16)[at] = pack_f16(v, scale.mul);
+      if (t < p.T && j == 0) p.t_scale[t] = scale.back;
     }
     if (p.dlp && out_here) {
       const size_t plane = (size_t)p.T * p.Epad / 8;
@@ -750,6 +776,7 @@ struct DxParams {
   int after_dw;           // the kernel before this one on the stream is dW's
   int spare_rows;         // rows of the sums that the spare warps take
   const float *t_scale;   // [T]
+  const float *w_scale;   // [H / 32]
   int *status;
 };
 
@@ -877,6 +904,10 @@ __global__ void __launch_bounds__(kDxThreads, 1)
       const int h = (int)(i / t_tiles), t0 = (int)(i - (long long)h * t_tiles) * kDxTok;
       const int tok0 = t0 + kDxTok / 2 * (int)rank + 32 * qd;
       const float scale = tok0 + lane < p.T ? __ldcg(p.t_scale + tok0 + lane) : 0.0f;
+      // of the warp's two 32 columns (H is a multiple of 128)
+      const int h0 = h * kTileH + col;
+      const float2 w_scale =
+          h0 < p.H ? __ldcg(reinterpret_cast<const float2 *>(p.w_scale + h0 / kWCols)) : make_float2(0.f, 0.f);
       const int buf = n & 1;
       if (!warp_wait(&s.acc_full[buf], (n >> 1) & 1u, lane, p.status)) break;
       tc_fence_after();
@@ -887,6 +918,7 @@ __global__ void __launch_bounds__(kDxThreads, 1)
       for (int c = 0; c < 2; ++c) {
         float v[32];
         tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * qd) << 16) + buf * 256 + col + 32 * c, v);
+        const float ws = c == 0 ? w_scale.x : w_scale.y;
         if (c == 1) {   // the accumulator is in registers
           tc_fence_before();
           __syncwarp();
@@ -897,14 +929,15 @@ __global__ void __launch_bounds__(kDxThreads, 1)
           uint32_t o[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            o[j] = bf162_bits(__floats2bfloat162_rn(v[8 * k + 2 * j] * scale, v[8 * k + 2 * j + 1] * scale));
+            // (one after the other: the product of the two may leave fp32's range)
+            o[j] = bf162_bits(__floats2bfloat162_rn(v[8 * k + 2 * j] * scale * ws,
+                                                    v[8 * k + 2 * j + 1] * scale * ws));
           *reinterpret_cast<uint4 *>(tile + lane * 128 + (((4 * c + k) ^ (lane & 7)) << 4)) =
               make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
       fence_async_smem();
       __syncwarp();
-      const int h0 = h * kTileH + col;   // H is a multiple of 128
       if (lane == 0 && h0 < p.H && tok0 < p.T) tma_store_2d(&map_dx, tile, h0, tok0);
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -1032,7 +1065,7 @@ __global__ void __launch_bounds__(kSmallThreads) route_grad_small_kernel(const R
   __syncthreads();
   if (p.dx) {   // (the limit of the other form: what is refused does not go by the batch)
     bool over = false;
-    for (int i = tid; i < E * kSmallH; i += kSmallThreads) over |= fabsf(ws[i]) * kWScale >= kF16Overflow;
+    for (int i = tid; i < E * kSmallH; i += kSmallThreads) over |= fabsf(ws[i]) >= kWLimit;
     if (over) set_status(p.status, STATUS_RANGE);
   }
   // dW: four experts of one h a thread; where that leaves threads over, the
@@ -1163,7 +1196,7 @@ int dw_pairs(int T, int E, int H) {
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct Layout {
-  size_t dlp, dl16, t_scale, w16, db, dw, total;
+  size_t dlp, dl16, t_scale, w16, w_scale, db, dw, total;
 };
 Layout layout(int T, int E, int H) {
   const int Epad = (E + 7) / 8 * 8;
@@ -1177,6 +1210,8 @@ Layout layout(int T, int E, int H) {
   off += up256((size_t)T * 4);
   L.w16 = off;
   off += up256((size_t)E * H * 2);
+  L.w_scale = off;
+  off += up256((size_t)H / kWCols * 4);
   L.db = off;
   off += up256((size_t)prep_blocks(T, 32) * E * 4);
   L.dw = off;
@@ -1239,11 +1274,10 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
   p.dl16 = p.dx ? reinterpret_cast<__half *>(w + L.dl16) : nullptr;
   p.t_scale = reinterpret_cast<float *>(w + L.t_scale);
   p.W16 = reinterpret_cast<__half *>(w + L.w16);
+  p.w_scale = reinterpret_cast<float *>(w + L.w_scale);
   p.db_part = p.db ? reinterpret_cast<float *>(w + L.db) : nullptr;
   p.dW_part = reinterpret_cast<float *>(w + L.dw);
-  const size_t n8 = (size_t)p.E * p.H / 8;
-  const int w_blocks =
-      p.dx ? (int)std::min<size_t>((n8 + 32 * kPrepWarps - 1) / (32 * kPrepWarps), 4 * kPairs) : 0;
+  const int w_blocks = p.dx ? p.H / kWCols : 0;
   cudaError_t e = launch_pdl(lanes == 8    ? route_grad_prep_kernel<8>
                              : lanes == 16 ? route_grad_prep_kernel<16>
                                            : route_grad_prep_kernel<32>,
@@ -1277,7 +1311,7 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
       return cudaErrorInvalidValue;
     const int fixed = (p.E + 63) / 64 * 2 * kDxWBox + kDxEpiWarps * kDxOut;
     DxParams d{p.T, p.H, p.E, std::min(kMaxStages, (kSmemLimit - 2048 - fixed) / kDxStage),
-               p.dW ? 1 : 0, 0, p.t_scale, p.status};
+               p.dW ? 1 : 0, 0, p.t_scale, p.w_scale, p.status};
     const int smem = fixed + d.stages * kDxStage + 1024;
     const long long items = (long long)((p.T + kDxTok - 1) / kDxTok) * tiles;
     // (pairs without an item of dx help with the sums, a row of 256 or an expert
