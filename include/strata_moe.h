@@ -527,16 +527,16 @@ strata_status strata_moe_balance_backward(strata_moe *h, const float *logits, in
  * its x: rows of x must be finite.  An expert named twice by a token gets both
  * terms.  x, dW, dx 16-byte aligned, workspace 256-byte aligned.  dW and db
  * are taken to fp32 accuracy (dl as three bf16 pieces on the tensor cores, fp32
- * sums in a fixed order); for dx, which is rounded to bf16, dl and W are rounded
- * to f16 (each token's dl and each 32 columns of W times a power of two first, so
- * whatever their size).  A dl
+ * sums in a fixed order); for dx, which is rounded to bf16, dl and W are taken to
+ * 22 bits (two f16 numbers, each token's dl and each 32 columns of W times a power
+ * of two first, so whatever their size).  A dl
  * that is not finite, or of magnitude above 3.3e38, gives NaN.  n_tokens == 0
  * zeroes dW and db.
  * dx must not be x.
  * Host errors: INVALID_ARG, CUDA.  Device errors: DEVICE_STATUS (bit 2: an id
  * outside [0, n_experts); that token's dw is ignored, as the forward's output
- * for it is zero), RANGE (a router weight of magnitude 65520 / 256 =
- * 255.9 or more, with dx). */
+ * for it is zero), RANGE (with dx, a router weight of magnitude
+ * 65520 / 256 = 255.9 or more; dx is computed all the same). */
 size_t strata_moe_route_backward_workspace(const strata_moe *h, int n_tokens);
 strata_status strata_moe_route_backward(strata_moe *h, const void *x_bf16, int n_tokens,
                                         const float *logits, const int32_t *idx, const float *dw,

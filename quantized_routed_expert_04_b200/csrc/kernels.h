@@ -158,9 +158,9 @@ struct RouteGradParams {
   int Epad, tok_blocks;
   int small_red;           // few tokens: offset of dW's parts in shared memory
   __nv_bfloat16 *dlp;      // [3][T][Epad] bf16 pieces of dl
-  __half *dl16;            // [T][Epad] dl / t_scale
+  __half *dl16;            // [2][T][Epad] dl / t_scale in two f16 parts
   float *t_scale;          // [T]
-  __half *W16;             // [E][H] W / w_scale
+  __half *W16;             // [2][E][H] W / w_scale in two f16 parts
   float *w_scale;          // [H / 32], one for 32 columns
   float *db_part;          // [tok_blocks][E]
   float *dW_part;          // parts of dW, [slot][E][256]

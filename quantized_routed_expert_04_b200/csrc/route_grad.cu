@@ -13,22 +13,26 @@
 // after dx the others, add up the parts of dW and db.  A few tokens take one launch on the fp32 units
 // instead (few_tokens below).
 //
-// 8192 tokens x 256 experts x 4096: 70 to 80 us of device time (alone and with cold
-// caches the preparation takes 12, dW 44, dx 28).  dW is bound by the tensor
-// cores, active for 87 % of the time on the multiprocessors that it uses (51.5
-// GFLOP for the three pieces, 33 us without the preparation and the sums); dx by
-// writing 67 MB.  2048 x 32 x 4096: 20 us, the latency of three launches over 35
-// MB.
+// 8192 tokens x 256 experts x 4096: 89 us replayed, 106 with fresh inputs (alone
+// and with caches flushed the preparation takes 13, dW 45, dx 44).  Both products
+// are bound by the tensor cores: 51.5 GFLOP each for three pieces, dW's on 64 of
+// the 74 pairs of blocks.  2048 x 32 x 4096: 20.6 us replayed, the latency of three
+// launches over 35 MB.
 //
 // fp32 operands on 16-bit tensor cores.  dW needs fp32 accuracy: x is bf16
 // already, and dl is taken as the sum of three bf16 numbers (its rounding, the
 // rounding of what is left, and again: 24 bits): three exact products per
-// element, added in fp32.  dx is rounded to bf16 (8 bits) at the end: dl and W
-// are rounded once to f16 (11 bits), each row of dl and each 32 columns of W
-// times the power of two that puts their largest magnitude in [2^14, 2^15), the
-// top of f16's range: whatever the sizes of the weights, what is lost below f16's
-// normal range is 2^-39 of the largest.  That is a third of the products that two
-// bf16 pieces of each would take.
+// element, added in fp32.  dx is rounded to bf16 at the end, but rows of dl that
+// come from a softmax sum to zero, so that whatever the rows of W have in common
+// cancels in dl W, and what a rounding of the operands loses of it does not: with
+// one f16 number (11 bits) for each, a common part of 16 times the rows' spread
+// made dx three times less exact than its last rounding, one of 64 eleven times.
+// So dl and W are two f16 numbers each (22 bits), three products per element (the
+// two small parts' left out): 18 us more than with one of 8192 tokens x 256 experts
+// x 4096, 0.6 to 1 with 32 experts.  Each row of dl and each 32 columns of W is first
+// multiplied by the power of two that puts its largest magnitude in [2^14, 2^15),
+// the top of f16's range: whatever the sizes of the weights, what is lost below
+// f16's normal range is 2^-39 of the largest.
 
 #include <cuda.h>
 
@@ -146,12 +150,12 @@ __device__ __forceinline__ float weight_grad(const RouteMode &mode, int id, floa
   return use ? slope * (dw - dot) : 0.0f;
 }
 
-// Eight floats -> f16.
-__device__ __forceinline__ uint4 pack_f16(const float v[8], float mul) {
-  return make_uint4(h2_bits(__floats2half2_rn(v[0] * mul, v[1] * mul)),
-                    h2_bits(__floats2half2_rn(v[2] * mul, v[3] * mul)),
-                    h2_bits(__floats2half2_rn(v[4] * mul, v[5] * mul)),
-                    h2_bits(__floats2half2_rn(v[6] * mul, v[7] * mul)));
+// Two floats -> their f16 roundings and those of what is left.
+__device__ __forceinline__ void split_f16(float a, float b, uint32_t &hi, uint32_t &lo) {
+  const __half2 h = __floats2half2_rn(a, b);
+  const float2 f = __half22float2(h);
+  hi = h2_bits(h);
+  lo = h2_bits(__floats2half2_rn(a - f.x, b - f.y));
 }
 // What takes a largest magnitude m to [2^14, 2^15), and back (m below 2^-112: as
 // far as a power of two goes, 2^126).
@@ -167,13 +171,13 @@ constexpr int kWCols = 32;             // columns of W that share a scale
 constexpr float kWLimit = kF16Overflow / 256.0f;
 
 // Blocks 0 .. tok_blocks - 1: rows of dl, a group of kG lanes per token, each lane
-// 8 consecutive experts, as three bf16 pieces and as scaled f16, and the block's
-// share of db.  The blocks behind them: 32 columns of W as scaled f16, all experts
+// 8 consecutive experts, as three bf16 pieces and as two of scaled f16, and the
+// block's share of db.  The blocks behind them: 32 columns of W likewise, all experts
 // in registers between the search for the largest and the rounding.  (kG holds the experts and the
 // selections; a warp per token whatever their number made the whole call over
 // 8192 tokens x 32 experts x 4096 take 44.1 us, 42.2 with 8 lanes each.)
 template <int kG>
-__global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const RouteGradParams p) {
+__global__ void __launch_bounds__(32 * kPrepWarps, 2) route_grad_prep_kernel(const RouteGradParams p) {
   constexpr int kTok = 32 / kG;   // tokens a warp works on at once
   // a row per group: the scattered selections, at the end the sums for db
   __shared__ __align__(16) float s_row[kPrepWarps * kTok][8 * kG];
@@ -204,10 +208,14 @@ __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const 
     const F16Scale scale = f16_scale(group_max(most[lane % kPrepWarps], kPrepWarps));
 #pragma unroll
     for (int k = 0; k < kTurns; ++k)
-      if (e0 + k * kRows < E)
-        *reinterpret_cast<uint2 *>(p.W16 + at + (size_t)k * kRows * p.H) =
-            make_uint2(h2_bits(__floats2half2_rn(v[k].x * scale.mul, v[k].y * scale.mul)),
-                       h2_bits(__floats2half2_rn(v[k].z * scale.mul, v[k].w * scale.mul)));
+      if (e0 + k * kRows < E) {
+        uint2 hi, lo;
+        split_f16(v[k].x * scale.mul, v[k].y * scale.mul, hi.x, lo.x);
+        split_f16(v[k].z * scale.mul, v[k].w * scale.mul, hi.y, lo.y);
+        __half *out = p.W16 + at + (size_t)k * kRows * p.H;
+        *reinterpret_cast<uint2 *>(out) = hi;
+        *reinterpret_cast<uint2 *>(out + (size_t)E * p.H) = lo;
+      }
     if (threadIdx.x == 0) p.w_scale[tile] = scale.back;
     if (over) set_status(p.status, STATUS_RANGE);
     return;
@@ -254,7 +262,16 @@ __global__ void __launch_bounds__(32 * kPrepWarps) route_grad_prep_kernel(const 
       for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
       m = group_max(m, kG);
       const F16Scale scale = f16_scale(m);
-      if (out_here) reinterpret_cast<uint4 *>(p.dl16)[at] = pack_f16(v, scale.mul);
+      if (out_here) {
+        uint4 hi, lo;
+        split_f16(v[0] * scale.mul, v[1] * scale.mul, hi.x, lo.x);
+        split_f16(v[2] * scale.mul, v[3] * scale.mul, hi.y, lo.y);
+        split_f16(v[4] * scale.mul, v[5] * scale.mul, hi.z, lo.z);
+        split_f16(v[6] * scale.mul, v[7] * scale.mul, hi.w, lo.w);
+        uint4 *out = reinterpret_cast<uint4 *>(p.dl16) + at;
+        out[0] = hi;
+        out[(size_t)p.T * p.Epad / 8] = lo;
+      }
       if (t < p.T && j == 0) p.t_scale[t] = scale.back;
     }
     if (p.dlp && out_here) {
@@ -757,22 +774,31 @@ __global__ void __launch_bounds__(256) route_grad_sum_kernel(const SumParams q) 
 }
 
 // dx[t][h] = sum_e dl[t][e] W[e][h]: M = 256 tokens, N = 256 rows of h, K = the
-// experts, in f16.  W's share of the tile (every expert) stays in shared memory
-// while tokens stream past it in stages of 64 experts.  Work items (h tile,
-// token tile), h-major, in one contiguous run per pair: W is loaded again only
-// where a run crosses into the next h tile.  The product itself is 16 MMAs an
-// item (2048 cycles with 256 experts), so writing dx counts: each lane scales
-// its token's row, writes bf16 to a swizzled tile, and bulk stores take it out.
+// experts, in f16: dl's large part by both parts of W, its small part by W's
+// large one.  W's share of the tile (every expert, both parts) stays in shared
+// memory while tokens stream past it in stages of 64 experts of one part.  Work
+// items (h tile, token tile), h-major, in one contiguous run per pair: W is loaded
+// again only where a run crosses into the next h tile.  With 256 experts an item
+// is 48 MMAs (6144 cycles), below 64 hardly any: there writing dx is what counts.
+// Each lane scales its token's row, writes bf16 to a swizzled tile of its warp, and
+// a bulk store takes the 64 h out; above 192 experts, where W leaves no room for
+// four stages of tokens beside such tiles, 32 h at a time.  (Stores straight from
+// registers, 32 bytes each: 8192 tokens x 32 experts x 4096 50.0 us, 44.1 this way;
+// with 256 experts the same.)  Every index is kept by adding: with a 64-bit
+// division for each item in every warp an item began 700 cycles later.
 constexpr int kDxTok = 256;
 constexpr int kDxStage = kDxTok / 2 * 128;   // per block
 constexpr int kDxWBox = 64 * 128;
-constexpr int kDxOut = 32 * 128;             // 32 tokens x 64 h of bf16
+constexpr int kDxOut = 32 * 64;              // 32 tokens x 32 h of bf16: half of a tile
 constexpr int kDxEpiWarps = 16;
 constexpr int kSumWarps = 4;
 constexpr int kDxThreads = 32 * (2 + kDxEpiWarps + kSumWarps);
 
 struct DxParams {
   int T, H, E, stages;
+  int out_halves;         // of a tile, per epilogue warp: 1 or 2
+  int t_tiles;            // of 256 tokens
+  int per, extra;         // items of a pair; that many pairs take one more
   int after_dw;           // the kernel before this one on the stream is dW's
   int spare_rows;         // rows of the sums that the spare warps take
   const float *t_scale;   // [T]
@@ -807,20 +833,25 @@ __global__ void __launch_bounds__(kDxThreads, 1)
   }
 
   const int n_kb = (p.E + 63) / 64;
-  const int t_tiles = (p.T + kDxTok - 1) / kDxTok;
-  const long long items = (long long)t_tiles * ((p.H + kTileH - 1) / kTileH);
-  const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
-  const long long i0 = run_begin(items, pairs, pair), i1 = run_begin(items, pairs, pair + 1);
-  uint8_t *w_smem = smem;                              // [k block][half of the block's 128 h]
-  uint8_t *ring = smem + n_kb * 2 * kDxWBox;
+  const int pair = blockIdx.x >> 1, items = p.per + (pair < p.extra);
+  const int first = pair * p.per + min(pair, p.extra);
+  int h = first / p.t_tiles, t = first - h * p.t_tiles;   // the item's tiles of h and of tokens
+  auto next_item = [&] {
+    if (++t == p.t_tiles) {
+      t = 0;
+      ++h;
+    }
+  };
+  uint8_t *w_smem = smem;                              // [part][k block][half of the block's 128 h]
+  const int w_part = n_kb * 2 * kDxWBox;
+  uint8_t *ring = smem + 2 * w_part;
   uint8_t *out_smem = ring + p.stages * kDxStage;      // [epilogue warp]
   if (warp == 0) {
     Ring r;
-    long long issued = 0;
-    int h = (int)(i0 / t_tiles), t = (int)(i0 - (long long)h * t_tiles), cur = -1, w_uses = 0;
+    int issued = 0, cur = -1, w_uses = 0;
     const uint32_t bar0 = cluster_addr(&s.full[0], 0), w_bar0 = cluster_addr(&s.w_full[0], 0);
     bool ok = true;
-    for (long long i = i0; i < i1 && ok; ++i) {
+    for (int n = 0; n < items && ok; ++n, next_item()) {
       const bool fresh = h != cur;
       if (fresh) {
         if (cur >= 0 && !warp_wait(&s.w_empty, (w_uses - 1) & 1u, lane, p.status)) { ok = false; break; }
@@ -829,29 +860,27 @@ __global__ void __launch_bounds__(kDxThreads, 1)
       }
       for (int kb = 0; kb < n_kb; ++kb) {
         if (fresh) {
-          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&s.w_full[kb], 4 * kDxWBox);
+          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&s.w_full[kb], 8 * kDxWBox);
           __syncwarp();
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
-            tma2_load_2d(w_smem + (kb * 2 + m) * kDxWBox, &map_w, h * kTileH + 128 * (int)rank + 64 * m,
-                         64 * kb, w_bar0 + 8 * kb);
+          for (int m = 0; m < 4; ++m)
+            tma2_load_3d(w_smem + (m / 2) * w_part + (kb * 2 + m % 2) * kDxWBox, &map_w,
+                         h * kTileH + 128 * (int)rank + 64 * (m % 2), 64 * kb, m / 2, w_bar0 + 8 * kb);
         }
-        if (ok && !warp_wait(&s.empty[r.st], r.ph ^ 1u, lane, p.status)) ok = false;
-        if (!ok) continue;   // (every copy of W that a barrier expects is still issued)
-        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&s.full[r.st], 2 * kDxStage);
-        __syncwarp();
-        tma2_load_2d(ring + r.st * kDxStage, &map_dl, 64 * kb, t * kDxTok + kDxTok / 2 * (int)rank,
-                     bar0 + 8 * r.st);
-        ++issued;
-        r.next(p.stages);
-      }
-      if (++t == t_tiles) {
-        t = 0;
-        ++h;
+        for (int part = 0; part < 2; ++part) {
+          if (ok && !warp_wait(&s.empty[r.st], r.ph ^ 1u, lane, p.status)) ok = false;
+          if (!ok) break;   // (every copy of W that a barrier expects is still issued)
+          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&s.full[r.st], 2 * kDxStage);
+          __syncwarp();
+          tma2_load_3d(ring + r.st * kDxStage, &map_dl, 64 * kb, t * kDxTok + kDxTok / 2 * (int)rank, part,
+                       bar0 + 8 * r.st);
+          ++issued;
+          r.next(p.stages);
+        }
       }
     }
     if (!ok && rank == 0 && lane == 0) {   // let issued copies land
-      for (long long m = issued > p.stages ? issued - p.stages : 0; m < issued; ++m)
+      for (int m = issued > p.stages ? issued - p.stages : 0; m < issued; ++m)
         (void)mbar_wait(&s.full[m % p.stages], (uint32_t)(m / p.stages) & 1u, p.status);
       for (int kb = 0; w_uses && kb < n_kb; ++kb) (void)mbar_wait(&s.w_full[kb], (w_uses - 1) & 1u, p.status);
     }
@@ -861,10 +890,9 @@ __global__ void __launch_bounds__(kDxThreads, 1)
       const uint32_t idesc = umma_idesc_16(false, kDxTok, kTileH, false, true);
       const uint64_t bd0 = umma_desc_mn_sw128(smem_u32(w_smem), kDxWBox);
       const uint64_t ad0 = umma_desc_sw128(smem_u32(ring));
-      int cur = -1, w_uses = 0, n = 0;
+      int cur = -1, w_uses = 0;
       bool ok = true;
-      for (long long i = i0; i < i1 && ok; ++i, ++n) {
-        const int h = (int)(i / t_tiles);
+      for (int n = 0; n < items && ok; ++n, next_item()) {
         const bool fresh = h != cur;
         if (fresh) {
           cur = h;
@@ -875,22 +903,28 @@ __global__ void __launch_bounds__(kDxThreads, 1)
         tc_fence_after();
         const uint32_t d = tmem + buf * 256;
         for (int kb = 0; kb < n_kb; ++kb) {
-          if ((fresh && !warp_wait(&s.w_full[kb], (w_uses - 1) & 1u, lane, p.status)) ||
-              !warp_wait(&s.full[r.st], r.ph, lane, p.status)) { ok = false; break; }
-          tc_fence_after();
+          if (fresh && !warp_wait(&s.w_full[kb], (w_uses - 1) & 1u, lane, p.status)) { ok = false; break; }
           const int steps = min(4, (p.E - 64 * kb + 15) / 16);
-          const uint64_t ad = ad0 + (uint64_t)(r.st * (kDxStage >> 4));
-          const uint64_t bd = bd0 + (uint64_t)(kb * (2 * kDxWBox >> 4));
+          const uint64_t bd = bd0 + (uint64_t)(kb * (2 * kDxWBox >> 4)), bd_lo = bd + (uint64_t)(w_part >> 4);
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            if (ks < steps)
-              umma2_f16(d, ad + ks * (32 >> 4), bd + ks * (2048 >> 4), idesc, kb > 0 || ks > 0 ? 1u : 0u);
-          umma2_commit(&s.empty[r.st]);
-          r.next(p.stages);
+          for (int part = 0; part < 2; ++part) {
+            if (!warp_wait(&s.full[r.st], r.ph, lane, p.status)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t ad = ad0 + (uint64_t)(r.st * (kDxStage >> 4));
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              if (ks < steps) {
+                umma2_f16(d, ad + ks * (32 >> 4), bd + ks * (2048 >> 4), idesc, part || kb > 0 || ks > 0 ? 1u : 0u);
+                if (part == 0) umma2_f16(d, ad + ks * (32 >> 4), bd_lo + ks * (2048 >> 4), idesc, 1u);
+              }
+            umma2_commit(&s.empty[r.st]);
+            r.next(p.stages);
+          }
+          if (!ok) break;
         }
         if (!ok) break;
         umma2_commit(&s.acc_full[buf]);
-        if (i + 1 < i1 && (int)((i + 1) / t_tiles) != cur) umma2_commit(&s.w_empty);
+        if (n + 1 < items && t + 1 == p.t_tiles) umma2_commit(&s.w_empty);
       }
     }
   } else if (warp < 2 + kDxEpiWarps) {
@@ -898,11 +932,10 @@ __global__ void __launch_bounds__(kDxThreads, 1)
     // tokens and 64 of the columns.
     const int qd = warp & 3, col = 64 * ((warp - 2) >> 2);
     const uint32_t empty_bar[2] = {cluster_addr(&s.acc_empty[0], 0), cluster_addr(&s.acc_empty[1], 0)};
-    uint8_t *tile = out_smem + (warp - 2) * kDxOut;
-    int n = 0;
-    for (long long i = i0; i < i1; ++i, ++n) {
-      const int h = (int)(i / t_tiles), t0 = (int)(i - (long long)h * t_tiles) * kDxTok;
-      const int tok0 = t0 + kDxTok / 2 * (int)rank + 32 * qd;
+    uint8_t *tile = out_smem + (warp - 2) * p.out_halves * kDxOut;
+    const bool half = p.out_halves == 1;
+    for (int n = 0; n < items; ++n, next_item()) {
+      const int tok0 = t * kDxTok + kDxTok / 2 * (int)rank + 32 * qd;
       const float scale = tok0 + lane < p.T ? __ldcg(p.t_scale + tok0 + lane) : 0.0f;
       // of the warp's two 32 columns (H is a multiple of 128)
       const int h0 = h * kTileH + col;
@@ -911,9 +944,6 @@ __global__ void __launch_bounds__(kDxThreads, 1)
       const int buf = n & 1;
       if (!warp_wait(&s.acc_full[buf], (n >> 1) & 1u, lane, p.status)) break;
       tc_fence_after();
-      // the tile's last store has read it
-      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-      __syncwarp();
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         float v[32];
@@ -924,6 +954,10 @@ __global__ void __launch_bounds__(kDxThreads, 1)
           __syncwarp();
           if (lane == 0) cluster_arrive(empty_bar[buf]);
         }
+        if (c == 0 || half) {   // the tile's last store has read it
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           uint32_t o[4];
@@ -932,13 +966,16 @@ __global__ void __launch_bounds__(kDxThreads, 1)
             // (one after the other: the product of the two may leave fp32's range)
             o[j] = bf162_bits(__floats2bfloat162_rn(v[8 * k + 2 * j] * scale * ws,
                                                     v[8 * k + 2 * j + 1] * scale * ws));
-          *reinterpret_cast<uint4 *>(tile + lane * 128 + (((4 * c + k) ^ (lane & 7)) << 4)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
+          const int at = half ? lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)
+                              : lane * 128 + (((4 * c + k) ^ (lane & 7)) << 4);
+          *reinterpret_cast<uint4 *>(tile + at) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        if (c == 1 || half) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0 && h0 < p.H && tok0 < p.T) tma_store_2d(&map_dx, tile, half ? h0 + 32 * c : h0, tok0);
         }
       }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0 && h0 < p.H && tok0 < p.T) tma_store_2d(&map_dx, tile, h0, tok0);
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     __syncwarp();
@@ -1205,11 +1242,11 @@ Layout layout(int T, int E, int H) {
   L.dlp = off;
   off += up256((size_t)3 * T * Epad * 2);
   L.dl16 = off;
-  off += up256((size_t)T * Epad * 2);
+  off += up256((size_t)2 * T * Epad * 2);
   L.t_scale = off;
   off += up256((size_t)T * 4);
   L.w16 = off;
-  off += up256((size_t)E * H * 2);
+  off += up256((size_t)2 * E * H * 2);
   L.w_scale = off;
   off += up256((size_t)H / kWCols * 4);
   L.db = off;
@@ -1220,18 +1257,20 @@ Layout layout(int T, int E, int H) {
   return L;
 }
 
-// 16-bit elements [planes][rows][cols], row stride ld elements, as boxes of 64 x
-// box_rows (one plane), 128-byte swizzle; elements outside read as zero.
+// 16-bit elements [planes][rows][cols], row stride ld elements, as boxes of
+// box_cols (64 or 32) x box_rows (one plane), swizzled over their 128 or 64 bytes;
+// elements outside read as zero.
 bool encode_planes(CUtensorMap *m, CUtensorMapDataType type, const void *base, int cols, int rows, int ld, int planes,
-                   int box_rows) {
+                   int box_cols, int box_rows) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
   cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * rows};
-  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, type, planes > 1 ? 3 : 2, const_cast<void *>(base), dims,
-             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1287,8 +1326,8 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
   if (e == cudaSuccess && p.dW) {
     CUtensorMap mx, md;
     const int form = p.E <= 64 ? 0 : p.E <= 128 ? 1 : 2, tok = dw_tok(p.E);
-    if (!encode_planes(&mx, kBf16, p.x, p.H, p.T, p.H, 1, tok) ||
-        !encode_planes(&md, kBf16, p.dlp, p.E, p.T, p.Epad, 3, tok))
+    if (!encode_planes(&mx, kBf16, p.x, p.H, p.T, p.H, 1, 64, tok) ||
+        !encode_planes(&md, kBf16, p.dlp, p.E, p.T, p.Epad, 3, 64, tok))
       return cudaErrorInvalidValue;
     const int stage = (2 + (form == 0 ? DwForm<0>::kBoxes : form == 1 ? DwForm<1>::kBoxes
                                                                       : DwForm<2>::kBoxes)) * tok * 128;
@@ -1304,22 +1343,25 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
   }
   const SumParams q{p, pairs, p.dW && tiles % pairs != 0 ? tiles * p.E : 0};
   if (e == cudaSuccess && p.dx) {
+    const int halves = p.E > 192 ? 1 : 2;
     CUtensorMap md, mw, mo;
-    if (!encode_planes(&md, kF16, p.dl16, p.E, p.T, p.Epad, 1, kDxTok / 2) ||
-        !encode_planes(&mw, kF16, p.W16, p.H, p.E, p.H, 1, 64) ||
-        !encode_planes(&mo, kBf16, p.dx, p.H, p.T, p.H, 1, 32))
+    if (!encode_planes(&md, kF16, p.dl16, p.E, p.T, p.Epad, 2, 64, kDxTok / 2) ||
+        !encode_planes(&mw, kF16, p.W16, p.H, p.E, p.H, 2, 64, 64) ||
+        !encode_planes(&mo, kBf16, p.dx, p.H, p.T, p.H, 1, halves == 1 ? 32 : 64, 32))
       return cudaErrorInvalidValue;
-    const int fixed = (p.E + 63) / 64 * 2 * kDxWBox + kDxEpiWarps * kDxOut;
-    DxParams d{p.T, p.H, p.E, std::min(kMaxStages, (kSmemLimit - 2048 - fixed) / kDxStage),
-               p.dW ? 1 : 0, 0, p.t_scale, p.w_scale, p.status};
+    const int fixed = (p.E + 63) / 64 * 4 * kDxWBox + kDxEpiWarps * halves * kDxOut;
+    const int t_tiles = (p.T + kDxTok - 1) / kDxTok, items = t_tiles * tiles;
+    DxParams d{p.T, p.H, p.E, std::min(kMaxStages, (kSmemLimit - 2048 - fixed) / kDxStage), halves, t_tiles,
+               0, 0, p.dW ? 1 : 0, 0, p.t_scale, p.w_scale, p.status};
     const int smem = fixed + d.stages * kDxStage + 1024;
-    const long long items = (long long)((p.T + kDxTok - 1) / kDxTok) * tiles;
     // (pairs without an item of dx help with the sums, a row of 256 or an expert
     // per warp; not many more than dW leaves room for, since those start late: 1024
     // tokens x 256 h x 256 experts 19.7 us with 64 pairs, 16.7 with 37)
     const int sums = sum_rows(q);
     const int help = std::min((sums + 2 * kSumWarps - 1) / (2 * kSumWarps), std::max(kPairs - pairs, kPairs / 2));
-    const int grid = (int)std::min<long long>(std::max<long long>(items, help), kPairs);
+    const int grid = std::min(std::max(items, help), kPairs);
+    d.per = items / grid;
+    d.extra = items % grid;
     // a row takes a spare warp about 1.2 us and an item of dx its pair 2.5: what the
     // spare warps would not have done by the end of dx, the epilogue's do then (2048
     // tokens x 1024 h x 256 experts: 20.0 us, 22.6 with the spare warps alone)

@@ -49,7 +49,9 @@ def check(W, dlogits, operand, what):
     (T, E), H = dlogits.shape, W.shape[1]
     x = normal(T, H, seed=1).bfloat16()
     dx, status = dx_of(W, x, dlogits)
-    assert int(status[0]) == 0, status
+    # (weights past the limit are reported, and dx is had all the same)
+    large = float(W.abs().max()) >= 65520 / 256
+    assert status == (binding.Status.RANGE, 16) if large else int(status[0]) == 0, status
     dl, w = dlogits.double(), W.double()
     want = dl @ w
     top = w.abs().view(E, H // 32, 32).amax((0, 2)).repeat_interleave(32)
@@ -76,3 +78,22 @@ def test_dx_of_columns_of_every_size(T, E, H):
     # and gradients whose rows are as far apart
     rows = 10.0 ** (torch.arange(T, device="cuda") % 16 - 8.0)
     check(normal(E, H, seed=4) * 1e-6, normal(T, E, seed=5) * rows[:, None], 2.0 ** -10 * (1 + 2.0 ** -9), "rows")
+
+
+# Rows of W with something in common, and rows of dl that sum to zero, as those of
+# a softmax do: what is common cancels, and what the operands' rounding loses of it
+# does not.  Each operand is two f16 numbers: 2^-22 relative each, and 2^-22 for the
+# product of the two small parts, which is left out; 16 u for 12 u and its squares.
+@pytest.mark.parametrize("T,E,H", SHAPES)
+@pytest.mark.parametrize("common", [0, 4, 64, 1000])
+def test_dx_of_router_weights_with_a_common_part(T, E, H, common):
+    W = (normal(E, H, seed=6) + common * normal(1, H, seed=7)) / math.sqrt(H)
+    p = torch.softmax(normal(T, E, seed=8), 1).double()
+    f = torch.rand(E, device="cuda", generator=gen(9)).double()
+    dlogits = (p * (f - p @ f[:, None])).float()
+    check(W, dlogits, 16 * U, "common %g" % common)
+    # and rows far from the others: one expert's, an eighth of them
+    W[0] *= 1e4
+    check(W, dlogits, 16 * U, "one large")
+    W[::8] *= -300
+    check(W, dlogits, 16 * U, "some large")
