@@ -251,6 +251,7 @@ __global__ void __launch_bounds__(32 * kPrepWarps, 2) route_grad_prep_kernel(con
       v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
       __syncwarp();
       if (first) row[in.id] = 0.0f;
+      __syncwarp();   // before another lane writes there: the next token's, or db's sums
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) db[i] += v[i];

@@ -762,3 +762,21 @@ def test_one_training_step_of_a_router(mode):
     for got, want, tol in zip((ds, dgain, out["dW"], out["db"]), grads, (2.0 ** -7, 2.0 ** -7, 1e-5, 1e-5)):
         assert float((got.double() - want).norm()) <= tol * float(want.norm())
     layer.close()
+
+
+# Consecutive tokens of a warp scatter to the same experts from other lanes, and the
+# last one's places become those of db's sums: without dx nothing else orders them.
+@pytest.mark.parametrize("T,E,k", [(2700, 64, 8), (2500, 128, 12), (1300, 256, 32), (9000, 8, 8)])
+@pytest.mark.parametrize("want", [("db",), ("dW", "db")])
+def test_route_backward_tokens_in_a_row_select_the_same_experts(T, E, k, want):
+    H = 256
+    x = acts(T, H, 181)
+    layer = make_layer(E, k, H=H)
+    logits, _ = routing(T, E, k, 182)
+    turn = torch.arange(T, device="cuda")[:, None] + torch.arange(k, device="cuda")
+    idx = (turn % k).int().contiguous()
+    dw = torch.randn(T, k, device="cuda", generator=gen(183))
+    for i in range(3):
+        check_route_backward(layer, x, None, logits, idx, dw, None, "softmax", want=want)
+        idx = (E - 1 - idx).contiguous()
+    layer.close()
