@@ -665,13 +665,16 @@ cudaError_t launch_norm_grad_as(NormGradParams p, cudaStream_t stream) {
   p.stages = 0;
   if (kVec) {
     // two blocks share a multiprocessor's 227 KB, or one takes it (a row of
-    // 16384 fp32 elements and its two gradients are 192 KB)
+    // 16384 fp32 elements and its two gradients are 192 KB).  The limit belongs to
+    // the kernel, not to the launch: every call sets the same one, so that calls of
+    // several threads do not lower it under one another.
+    constexpr int kLimit = (kMinBlocks > 1 ? 110 : 220) * 1024;
+    constexpr int kMostH = kTpr * kNe;
+    static_assert(kRows * kMostH * 3 * (int)sizeof(T) <= kLimit, "one stage of the widest rows fits");
     const int stage = p.H * (int)sizeof(T) * (p.dsum ? 3 : 2);
-    p.stages = std::min(kMaxStages, std::max(1, (kMinBlocks > 1 ? 110 : 220) * 1024 / (kRows * stage)));
+    p.stages = std::min(kMaxStages, kLimit / (kRows * stage));
     smem = std::max(smem, kRows * p.stages * stage);
-  }
-  if (smem > 0) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLimit);
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(kern, dim3(grad_blocks(p.T, p.H)), dim3(kTpr * kRows), smem, stream, p);

@@ -1184,6 +1184,11 @@ __global__ void __launch_bounds__(kSmallThreads) route_grad_small_kernel(const R
 
 // ---------------------------------------------------------------- host
 constexpr int kPairs = 74;   // 148 multiprocessors
+// Limits of dynamic shared memory, the same in every call whatever it needs: they
+// belong to the kernel, and calls of several threads must not lower them under one
+// another.
+constexpr int kTcSmem = kSmemLimit - 1024;
+constexpr int kSmallSmem = 116 * 1024;
 static_assert(4 * kPairs <= 320, "sum_db reads up to 320 blocks' parts");
 
 // Lanes of the preparation per token: the power of two that holds the experts, 8 a
@@ -1301,7 +1306,7 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
     const int smem = (int)layout.total, hs = small_hs(p.H);
     p.small_red = (int)layout.red;
     auto kern = hs == 16 ? route_grad_small_kernel<16> : route_grad_small_kernel<32>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(p.H / hs), dim3(kSmallThreads), smem, stream, p);
   }
@@ -1338,7 +1343,7 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
     auto kern = form == 0   ? route_grad_dw_kernel<0>
                 : form == 1 ? route_grad_dw_kernel<1>
                             : route_grad_dw_kernel<2>;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
     if (e == cudaSuccess)
       e = launch_pdl_cluster(kern, dim3(2 * pairs), 2, dim3(kTcThreads), smem, stream, d, mx, md);
   }
@@ -1367,7 +1372,7 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
     // spare warps would not have done by the end of dx, the epilogue's do then (2048
     // tokens x 1024 h x 256 experts: 20.0 us, 22.6 with the spare warps alone)
     d.spare_rows = (int)std::min<long long>(sums, 2LL * grid * kSumWarps * (1 + 2 * (items / grid)));
-    e = cudaFuncSetAttribute(route_grad_dx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(route_grad_dx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
     if (e == cudaSuccess)
       e = launch_pdl_cluster(route_grad_dx_kernel, dim3(2 * grid), 2, dim3(kDxThreads), smem, stream, d, q, md, mw, mo);
   } else if (e == cudaSuccess && sum_rows(q)) {
