@@ -48,6 +48,7 @@ __global__ void combine_kernel(const float *y, const int32_t *idx, const float *
 // One work item = (active expert, group of <= 16 of its pairs, one 16-row
 // weight tile: 8 gate + 8 up rows, or 16 down rows).
 constexpr int kFusedWarps = 16;                     // warps per CTA, each with its own ring
+constexpr int kFusedSmem = 232448;                  // bytes of shared memory per CTA, at most
 constexpr int kMmMaxStages = 8;                     // stages per warp ring
 constexpr int kMmMaxGroup = 16;                     // pairs per item (two n8 MMA tiles)
 constexpr int kMmSlotFloats = kMmMaxGroup * 16;     // partial sums of one piece: pairs x rows

@@ -392,7 +392,7 @@ strata_status run_fused(strata_moe *h, const void *x, int T, const int32_t *idx_
   p.stage_bytes = (int)align_up((size_t)p.kc * 9, 128);
   const size_t tables = fused_table_bytes(T, h->k, h->S);
   const size_t bars = (size_t)kFusedWarps * kMmMaxStages * sizeof(uint64_t);
-  const size_t avail = 232448 - tables - bars;
+  const size_t avail = kFusedSmem - tables - bars;
   p.stages = (int)std::min<size_t>(kMmMaxStages, avail / ((size_t)kFusedWarps * p.stage_bytes));
   if (p.stages < 2) return STRATA_ERR_UNSUPPORTED;
   p.smem_tables = (size_t)kFusedWarps * p.stages * p.stage_bytes + bars;
@@ -415,8 +415,9 @@ strata_status run_fused(strata_moe *h, const void *x, int T, const int32_t *idx_
                   ? (p.group <= 8 ? decode_fused_kernel<1, kFmtInt4> : decode_fused_kernel<2, kFmtInt4>)
                   : (p.group <= 8 ? decode_fused_kernel<1, kFmtNvfp4>
                                   : decode_fused_kernel<2, kFmtNvfp4>);
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // (the same limit whatever this call needs: it belongs to the kernel, and calls
+  // of several threads must not lower it under one another)
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFusedSmem);
   if (e != cudaSuccess) return cuda_status(e);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(h->num_sms);

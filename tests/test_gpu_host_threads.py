@@ -83,3 +83,26 @@ def test_router_gradient_of_two_sizes(shapes):
     for layer in layers:
         assert int(layer.status()[0]) == 0
         layer.close()
+
+
+def test_decode_of_two_batches():
+    from harness import GpuLayer
+    from quantized_routed_expert_04_b200 import synth
+    L = binding.load_library()
+    layers = [GpuLayer(synth.CONFIGS["tiny"]) for _ in range(2)]
+
+    def call(gl, T):
+        x = torch.randn(T, gl.cfg.hidden, device="cuda").bfloat16()
+        out = torch.empty_like(x)
+        gl.layer.reserve(T)
+
+        def run(stream):
+            st = L.strata_moe_forward(gl.layer.h, x.data_ptr(), T, out.data_ptr(), stream)
+            if st:
+                raise binding.StrataError(st, "strata_moe_forward %d" % T)
+        return run
+
+    both(call(layers[0], 9), call(layers[1], 64))
+    for gl in layers:
+        assert int(gl.layer.status()[0]) == 0
+        gl.close()
