@@ -286,11 +286,28 @@ def _rows(t, shape, dtype, dev, where):
     return t.data_ptr(), ld
 
 
-def _flat(t, dev, nbytes, where):
-    """Address of a contiguous operand of nbytes bytes."""
+# The types that an operand of a kind may have (torch's, known once a tensor has
+# come).
+_BF16, _F32, _I32, _BYTES, _E4M3 = [], [], [], [], []
+
+
+def _of_kind(t, kind):
+    if not _F32:
+        torch = _get_torch()
+        _BF16.append(torch.bfloat16)
+        _I32.append(torch.int32)
+        _BYTES.extend((torch.uint8, torch.bool))
+        _E4M3.extend((torch.float8_e4m3fn, torch.uint8))
+        _F32.append(torch.float32)
+    return t.dtype in kind
+
+
+def _flat(t, dev, nbytes, kind, where):
+    """Address of a contiguous operand of nbytes bytes and of one of the kind's types."""
     if t is None:
         return 0
-    if t.nbytes != nbytes or t.get_device() != dev or not t.is_contiguous():
+    if (t.nbytes != nbytes or t.get_device() != dev or not t.is_contiguous() or
+            t.dtype not in kind and not _of_kind(t, kind)):
         _refuse(where)
     return t.data_ptr()
 
@@ -302,11 +319,6 @@ def _workspace(t, dev, where):
     if t.get_device() != dev or not t.is_contiguous():
         _refuse(where)
     return t.data_ptr(), t.nbytes
-
-
-def _bf16(t, where):
-    if t is not None and t.dtype is not (_torch or _get_torch()).bfloat16:
-        _refuse(where)
 
 
 def _stream_on(stream, dev, where):
@@ -356,9 +368,9 @@ def strata_rmsnorm(x, residual, weight, eps, residual_out=None, out=None, out_q8
     if out_q8 is not None:
         if group <= 0 or scales is None:
             _refuse(w)
-        qa = _flat(out_q8, dev, T * H, w)
-        sa = _flat(scales, dev, T * -(-H // group) * 4, w)
-    wa = _flat(weight, dev, H * 4, w)
+        qa = _flat(out_q8, dev, T * H, _E4M3, w)
+        sa = _flat(scales, dev, T * -(-H // group) * 4, _F32, w)
+    wa = _flat(weight, dev, H * 4, _F32, w)
     _packed_rmsnorm(w, _dtype(x), xa, ldx, ra, ldr, wa, eps, T, H, roa, ldro, oa, ldo, qa, sa, group,
                     _stream_on(stream, dev, w))
 
@@ -378,7 +390,7 @@ def strata_rmsnorm_backward(h, weight, eps, dout, dsum, dx, dweight=None, worksp
     da, ldd = _rows(dout, shape, dt, dev, w)
     sa, lds = _rows(dsum, shape, dt, dev, w)
     xa, ldx = _rows(dx, shape, dt, dev, w)
-    wa, dwa = _flat(weight, dev, H * 4, w), _flat(dweight, dev, H * 4, w)
+    wa, dwa = _flat(weight, dev, H * 4, _F32, w), _flat(dweight, dev, H * 4, _F32, w)
     ws, nws = _workspace(workspace, dev, w)
     _packed_rmsnorm_backward(w, _dtype(h), ha, ldh, wa, eps, da, ldd, sa, lds, T, H, xa, ldx, dwa,
                              ws, nws, _stream_on(stream, dev, w))
@@ -558,24 +570,21 @@ class StrataMoE:
     # (StrataError, INVALID_ARG).
     def forward_norm(self, x, residual, weight, eps, residual_out, normed, out, stream=None):
         w = "strata_moe_forward_norm"
-        for t in (x, residual, residual_out, normed, out):
-            _bf16(t, w)
         T, dev = x.shape[0], x.get_device()
         n = T * self.hidden * 2
-        a = [_flat(t, dev, n, w) for t in (x, residual, residual_out, normed, out)]
-        wa = _flat(weight, dev, self.hidden * 4, w)
+        a = [_flat(t, dev, n, _BF16, w) for t in (x, residual, residual_out, normed, out)]
+        wa = _flat(weight, dev, self.hidden * 4, _F32, w)
         strata_moe_forward_norm(self.h, a[0], a[1], wa, eps, T, a[2], a[3], a[4],
                                 _stream_on(stream, dev, w))
 
     def forward_q8(self, x_q8, scales, group, x, out, stream=None):
         w = "strata_moe_forward_q8"
         T, H, dev = x_q8.shape[0], self.hidden, x_q8.get_device()
-        _bf16(x, w)
-        _bf16(out, w)
         if group <= 0:
             _refuse(w)
-        qa, sa = _flat(x_q8, dev, T * H, w), _flat(scales, dev, T * -(-H // group) * 4, w)
-        xa, oa = _flat(x, dev, T * H * 2, w), _flat(out, dev, T * H * 2, w)
+        qa = _flat(x_q8, dev, T * H, _E4M3, w)
+        sa = _flat(scales, dev, T * -(-H // group) * 4, _F32, w)
+        xa, oa = _flat(x, dev, T * H * 2, _BF16, w), _flat(out, dev, T * H * 2, _BF16, w)
         strata_moe_forward_q8(self.h, qa, sa, group, T, xa, oa, _stream_on(stream, dev, w))
 
     # Training the router; `workspace` is a buffer of the size that the
@@ -588,10 +597,10 @@ class StrataMoE:
         w = "strata_moe_balance"
         T, E, dev = logits.shape[0], self.n_experts, logits.get_device()
         n_seq = 1 if seq_off is None else seq_off.numel() - 1
-        la, ia = _flat(logits, dev, T * E * 4, w), _flat(idx, dev, T * self.top_k * 4, w)
-        ca, ta = _flat(counts, dev, n_seq * E * 4, w), _flat(tokens, dev, n_seq * 4, w)
-        sa, ma = _flat(seq_off, dev, n_seq * 4 + 4, w), _flat(mask, dev, T, w)
-        loa = _flat(loss, dev, 4, w)
+        la, ia = _flat(logits, dev, T * E * 4, _F32, w), _flat(idx, dev, T * self.top_k * 4, _I32, w)
+        ca, ta = _flat(counts, dev, n_seq * E * 4, _I32, w), _flat(tokens, dev, n_seq * 4, _I32, w)
+        sa, ma = _flat(seq_off, dev, n_seq * 4 + 4, _I32, w), _flat(mask, dev, T, _BYTES, w)
+        loa = _flat(loss, dev, 4, _F32, w)
         ws, nws = _workspace(workspace, dev, w)
         _packed_balance(w, self.h, la, ia, T, sa, n_seq, ma, coef, ca, ta, loa, ws, nws,
                         _stream_on(stream, dev, w))
@@ -601,10 +610,10 @@ class StrataMoE:
         w = "strata_moe_balance_backward"
         T, E, dev = logits.shape[0], self.n_experts, logits.get_device()
         n_seq = 1 if seq_off is None else seq_off.numel() - 1
-        la, da = _flat(logits, dev, T * E * 4, w), _flat(dlogits, dev, T * E * 4, w)
-        ca, ta = _flat(counts, dev, n_seq * E * 4, w), _flat(tokens, dev, n_seq * 4, w)
-        sa, ma = _flat(seq_off, dev, n_seq * 4 + 4, w), _flat(mask, dev, T, w)
-        dla = _flat(dloss, dev, 4, w)
+        la, da = _flat(logits, dev, T * E * 4, _F32, w), _flat(dlogits, dev, T * E * 4, _F32, w)
+        ca, ta = _flat(counts, dev, n_seq * E * 4, _I32, w), _flat(tokens, dev, n_seq * 4, _I32, w)
+        sa, ma = _flat(seq_off, dev, n_seq * 4 + 4, _I32, w), _flat(mask, dev, T, _BYTES, w)
+        dla = _flat(dloss, dev, 4, _F32, w)
         _packed_balance_backward(w, self.h, la, T, sa, n_seq, ma, coef, ca, ta, dla, da,
                                  _stream_on(stream, dev, w))
 
@@ -613,14 +622,12 @@ class StrataMoE:
 
     def route_backward(self, x, logits, idx, dw, dlogits, dW, db, dx, workspace, stream=None):
         w = "strata_moe_route_backward"
-        _bf16(x, w)
-        _bf16(dx, w)
         T, dev = x.shape[0], x.get_device()
         E, k, H = self.n_experts, self.top_k, self.hidden
-        xa, dxa = _flat(x, dev, T * H * 2, w), _flat(dx, dev, T * H * 2, w)
-        la, dla = _flat(logits, dev, T * E * 4, w), _flat(dlogits, dev, T * E * 4, w)
-        ia, dwa = _flat(idx, dev, T * k * 4, w), _flat(dw, dev, T * k * 4, w)
-        dWa, dba = _flat(dW, dev, E * H * 4, w), _flat(db, dev, E * 4, w)
+        xa, dxa = _flat(x, dev, T * H * 2, _BF16, w), _flat(dx, dev, T * H * 2, _BF16, w)
+        la, dla = _flat(logits, dev, T * E * 4, _F32, w), _flat(dlogits, dev, T * E * 4, _F32, w)
+        ia, dwa = _flat(idx, dev, T * k * 4, _I32, w), _flat(dw, dev, T * k * 4, _F32, w)
+        dWa, dba = _flat(dW, dev, E * H * 4, _F32, w), _flat(db, dev, E * 4, _F32, w)
         ws, nws = _workspace(workspace, dev, w)
         _packed_route_backward(w, self.h, xa, T, la, ia, dwa, dla, dWa, dba, dxa, ws, nws,
                                _stream_on(stream, dev, w))
