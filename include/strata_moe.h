@@ -390,9 +390,9 @@ enum { STRATA_DTYPE_BF16 = 0, STRATA_DTYPE_F16 = 1, STRATA_DTYPE_F32 = 2 };
  * `dtype`, row t starting at element t * stride (strides in elements, >= hidden;
  * ignored for one row).  residual may be NULL (s = x); residual_out (receives
  * s) may be NULL; out (receives y) may be NULL if out_q8 is given.  weight:
- * device fp32 [hidden].  residual_out may be x or residual, and out any of the
- * three inputs, in the same place (same address and stride); residual_out and
- * out must not overlap.
+ * device fp32 [hidden].  residual_out may be x or residual, and out too, in
+ * the same place (same address and stride); otherwise an output that shares
+ * elements with another row operand is refused.
  * out_q8 (or NULL): device e4m3 [n_tokens][hidden], contiguous, with one fp32
  * scale per `group` consecutive columns of a row, scales [n_tokens]
  * [ceil(hidden / group)]: scale = max(largest |y| of the group / 448, 2^-126),
@@ -415,7 +415,7 @@ strata_status strata_rmsnorm(int dtype, const void *x, long long x_stride, const
  *     dx = i * gy - h * i^3 * mean(gy * h) + dsum
  *     dweight = sum over tokens of dout * h * i
  * dx (type `dtype`) is the gradient of both x and residual; it may be h, dout
- * or dsum in the same place.  dweight: device fp32 [hidden], or NULL.  The sums
+ * or dsum in the same place and is refused where it shares elements otherwise.  dweight: device fp32 [hidden], or NULL.  The sums
  * are taken in a fixed order: the same inputs give the same bits.
  * workspace: device memory of strata_rmsnorm_backward_workspace bytes, 16-byte
  * aligned, written before it is read; NULL if dweight is.  Calls that may

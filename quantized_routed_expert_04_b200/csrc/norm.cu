@@ -15,6 +15,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <cstdlib>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -736,6 +737,27 @@ inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_
 bool rows_ok(const void *p, long long ld, int T, int H, int bytes) {
   return p && aligned(p, bytes) && (T <= 1 || ld >= H);
 }
+// Two row operands, one of them written, share elements other than by being in the
+// same place (where each row is read before it is written): a block would write
+// what another has yet to read.
+bool rows_clash(const void *a, long long lda, const void *b, long long ldb, int T, int H, int bytes) {
+  if (!a || !b) return false;
+  if (T <= 1) lda = ldb = H;
+  if (a == b && lda == ldb) return false;
+  const long long d = (long long)(reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a));
+  const long long row = (long long)H * bytes, sa = lda * bytes, sb = ldb * bytes;
+  if (d >= (T - 1) * sa + row || -d >= (T - 1) * sb + row) return false;   // one ends before the other begins
+  // row i of a begins i sa behind a's start and meets row j of b if |d + j sb - i sa|
+  // is less than a row: with one stride that goes by i - j alone
+  const int rows = sa == sb ? 1 : T;
+  for (int i = 0; i < rows; ++i) {
+    const long long at = i * sa - d;   // from b's start
+    long long j = at >= 0 ? at / sb : -((-at + sb - 1) / sb);   // the row of b at or before it
+    for (int k = 0; k < 2; ++k, ++j)
+      if (llabs(at - j * sb) < row && (sa == sb ? llabs(j) < T : j >= 0 && j < T)) return true;
+  }
+  return false;
+}
 // ... that 16-byte accesses can walk.
 bool rows_vec(const void *p, long long ld, int bytes) {
   return !p || (aligned(p, 16) && ld * bytes % 16 == 0);
@@ -777,6 +799,14 @@ strata_status strata_rmsnorm(int dtype, const void *x, long long x_stride, const
   if ((residual && !rows_ok(residual, residual_stride, n_tokens, hidden, b)) ||
       (residual_out && !rows_ok(residual_out, residual_out_stride, n_tokens, hidden, b)) ||
       (out && !rows_ok(out, out_stride, n_tokens, hidden, b)))
+    return STRATA_ERR_INVALID_ARG;
+  auto clash = [&](const void *u, long long ldu, const void *v, long long ldv) {
+    return rows_clash(u, ldu, v, ldv, n_tokens, hidden, b);
+  };
+  if (clash(residual_out, residual_out_stride, x, x_stride) ||
+      clash(residual_out, residual_out_stride, residual, residual_stride) ||
+      clash(residual_out, residual_out_stride, out, out_stride) || clash(out, out_stride, x, x_stride) ||
+      clash(out, out_stride, residual, residual_stride))
     return STRATA_ERR_INVALID_ARG;
   NormParams p;
   p.x = x;
@@ -837,6 +867,10 @@ strata_status strata_rmsnorm_backward(int dtype, const void *h, long long h_stri
       !rows_ok(dout, dout_stride, n_tokens, hidden, b) ||
       (dsum && !rows_ok(dsum, dsum_stride, n_tokens, hidden, b)) ||
       !rows_ok(dx, dx_stride, n_tokens, hidden, b))
+    return STRATA_ERR_INVALID_ARG;
+  if (rows_clash(dx, dx_stride, h, h_stride, n_tokens, hidden, b) ||
+      rows_clash(dx, dx_stride, dout, dout_stride, n_tokens, hidden, b) ||
+      rows_clash(dx, dx_stride, dsum, dsum_stride, n_tokens, hidden, b))
     return STRATA_ERR_INVALID_ARG;
   if (dweight && (!workspace || !aligned(workspace, 16) ||
                   workspace_bytes < strata_rmsnorm_backward_workspace(n_tokens, hidden)))
