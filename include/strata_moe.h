@@ -433,8 +433,8 @@ strata_status strata_rmsnorm_backward(int dtype, const void *h, long long h_stri
  * strata_rmsnorm in bf16, then strata_moe_forward of x'.  x_bf16,
  * residual_bf16 (or NULL), residual_out_bf16 (or NULL), normed_bf16 (receives
  * x', 16-byte aligned; it is also the x of strata_moe_route_backward) and
- * out_bf16: device bf16 [n_tokens][hidden], contiguous; out must be none of the
- * other outputs.  residual_out may be x or residual.  Runs on the handle's
+ * out_bf16: device bf16 [n_tokens][hidden], contiguous; out must share no
+ * memory with the other outputs.  residual_out may be x or residual.  Runs on the handle's
  * device, which must be the current one.  Errors: those of strata_rmsnorm and
  * strata_moe_forward. */
 strata_status strata_moe_forward_norm(strata_moe *h, const void *x_bf16, const void *residual_bf16,
@@ -446,8 +446,8 @@ strata_status strata_moe_forward_norm(strata_moe *h, const void *x_bf16, const v
  * bytes of bf16 where rows travel between the norm and the layer): x_q8 device
  * e4m3 [n_tokens][hidden], 16-byte aligned, scales device fp32 [n_tokens]
  * [ceil(hidden / group)], group 32, 64, 128 or >= hidden.  x_bf16 (device bf16
- * [n_tokens][hidden], 16-byte aligned) receives q * scale, rounded once, and
- * the result is strata_moe_forward's of it.  Runs on the handle's device, which
+ * [n_tokens][hidden], 16-byte aligned, sharing no memory with x_q8 or out)
+ * receives q * scale, rounded once, and the result is strata_moe_forward's of it.  Runs on the handle's device, which
  * must be the current one.  Errors: as strata_moe_forward. */
 strata_status strata_moe_forward_q8(strata_moe *h, const void *x_q8, const float *scales, int group,
                                     int n_tokens, void *x_bf16, void *out_bf16,
@@ -501,7 +501,8 @@ strata_status strata_moe_balance(strata_moe *h, const float *logits, const int32
  *     sigmoid: dlogits[t][e] = u s_e (1 - s_e) / S (f_e - sum_j f_j p_j)
  * and zero for tokens that do not count (masked, or outside every sequence).
  * counts and tokens: as strata_moe_balance wrote them; dloss: device fp32 [1],
- * or NULL for 1; dlogits: device fp32 [n_tokens][n_experts], not logits.  No
+ * or NULL for 1; dlogits: device fp32 [n_tokens][n_experts], none of
+ * it in logits.  No
  * workspace.  Errors: INVALID_ARG, CUDA. */
 strata_status strata_moe_balance_backward(strata_moe *h, const float *logits, int n_tokens,
                                           const int32_t *seq_off, int n_seq, const uint8_t *mask,
@@ -532,7 +533,7 @@ strata_status strata_moe_balance_backward(strata_moe *h, const float *logits, in
  * of two first, so whatever their size).  A dl
  * that is not finite, or of magnitude above 3.3e38, gives NaN.  n_tokens == 0
  * zeroes dW and db.
- * dx must not be x.
+ * dx must not share memory with x.
  * Host errors: INVALID_ARG, CUDA.  Device errors: DEVICE_STATUS (bit 2: an id
  * outside [0, n_experts); that token's dw is ignored, as the forward's output
  * for it is zero), RANGE (with dx, a router weight of magnitude

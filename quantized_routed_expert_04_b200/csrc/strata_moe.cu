@@ -665,6 +665,12 @@ strata_status strata_moe_route(strata_moe *h, const void *x_bf16, int n_tokens, 
                     stream);
 }
 
+// Two ranges of memory share bytes.
+static bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const auto u = reinterpret_cast<uintptr_t>(a), v = reinterpret_cast<uintptr_t>(b);
+  return a && b && u < v + nb && v < u + na;
+}
+
 // What strata_moe_forward refuses.
 static strata_status check_layer_input(const strata_moe *h, const void *x_bf16, int n_tokens,
                                        const void *out_bf16) {
@@ -720,7 +726,9 @@ strata_status strata_moe_forward_norm(strata_moe *h, const void *x_bf16, const v
   if (cudaGetDevice(&device) != cudaSuccess) return STRATA_ERR_CUDA;
   if (device != h->device) return STRATA_ERR_INVALID_ARG;
   if (n_tokens == 0) return STRATA_OK;
-  if (out_bf16 == normed_bf16 || out_bf16 == residual_out_bf16) return STRATA_ERR_INVALID_ARG;
+  const size_t bytes = sizeof(__nv_bfloat16) * (size_t)n_tokens * h->H;
+  if (overlap(out_bf16, bytes, normed_bf16, bytes) || overlap(out_bf16, bytes, residual_out_bf16, bytes))
+    return STRATA_ERR_INVALID_ARG;
   // before the norm is enqueued, so that a refused call enqueues nothing
   st = grow_workspace(h, n_tokens);
   if (st != STRATA_OK) return st;
@@ -740,8 +748,10 @@ strata_status strata_moe_forward_q8(strata_moe *h, const void *x_q8, const float
   if (cudaGetDevice(&device) != cudaSuccess) return STRATA_ERR_CUDA;
   if (device != h->device) return STRATA_ERR_INVALID_ARG;
   if (n_tokens == 0) return STRATA_OK;
+  const size_t n = (size_t)n_tokens * h->H;
   if (!x_q8 || (reinterpret_cast<uintptr_t>(x_q8) & 15) || !scales ||
-      (reinterpret_cast<uintptr_t>(scales) & 3) || out_bf16 == x_bf16)
+      (reinterpret_cast<uintptr_t>(scales) & 3) || overlap(out_bf16, 2 * n, x_bf16, 2 * n) ||
+      overlap(x_bf16, 2 * n, x_q8, n))
     return STRATA_ERR_INVALID_ARG;
   st = grow_workspace(h, n_tokens);
   if (st != STRATA_OK) return st;
@@ -897,8 +907,10 @@ strata_status strata_moe_balance_backward(strata_moe *h, const float *logits, in
   strata_status st = check_balance(h, logits, n_tokens, seq_off, n_seq, coef, counts, tokens);
   if (st != STRATA_OK) return st;
   if (misaligned(dloss, 4)) return STRATA_ERR_INVALID_ARG;
-  if (n_tokens > 0 && (!dlogits || misaligned(dlogits, 4) || dlogits == logits))
+  if (n_tokens > 0 && (!dlogits || misaligned(dlogits, 4)))
     return STRATA_ERR_INVALID_ARG;
+  const size_t bytes = sizeof(float) * (size_t)n_tokens * h->E;
+  if (overlap(dlogits, bytes, logits, bytes)) return STRATA_ERR_INVALID_ARG;
   st = check_device(h);
   if (st != STRATA_OK) return st;
   if (n_tokens == 0) return STRATA_OK;
@@ -930,8 +942,7 @@ strata_status strata_moe_route_backward(strata_moe *h, const void *x_bf16, int n
                                         const float *dlogits, float *dW, float *db, void *dx_bf16,
                                         void *workspace, size_t workspace_bytes,
                                         strata_stream_t stream) {
-  if (!h || n_tokens < 0 || n_tokens > kMaxTrainTokens || (!dW && !db && !dx_bf16) ||
-      (dx_bf16 && dx_bf16 == x_bf16))
+  if (!h || n_tokens < 0 || n_tokens > kMaxTrainTokens || (!dW && !db && !dx_bf16))
     return STRATA_ERR_INVALID_ARG;
   if (misaligned(dW, 16) || misaligned(db, 4) || misaligned(dx_bf16, 16)) return STRATA_ERR_INVALID_ARG;
   if (n_tokens > 0) {
@@ -940,6 +951,9 @@ strata_status strata_moe_route_backward(strata_moe *h, const void *x_bf16, int n
       return STRATA_ERR_INVALID_ARG;
     if ((dW && (!x_bf16 || misaligned(x_bf16, 16))) || (dx_bf16 && !h->router_W))
       return STRATA_ERR_INVALID_ARG;
+    // (dx may be written while dW still reads x)
+    const size_t bytes = sizeof(__nv_bfloat16) * (size_t)n_tokens * h->H;
+    if (overlap(dx_bf16, bytes, x_bf16, bytes)) return STRATA_ERR_INVALID_ARG;
     if (!workspace || misaligned(workspace, 256) ||
         workspace_bytes < route_grad_workspace(n_tokens, h->E, h->H))
       return STRATA_ERR_INVALID_ARG;
