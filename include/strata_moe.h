@@ -485,8 +485,8 @@ strata_status strata_moe_forward_q8(strata_moe *h, const void *x_q8, const float
  * order.  n_tokens == 0 zeroes the outputs.  Asynchronous on `stream`.
  * Host errors: INVALID_ARG, CUDA.  Device errors (strata_moe_get_status):
  * DEVICE_STATUS (bit 2: an id of a counting token outside [0, n_experts), not
- * counted; bit 8: seq_off decreasing or outside [0, n_tokens], the sequence's
- * span is clamped). */
+ * counted; bit 8: seq_off outside [0, n_tokens], where the sequence's span is
+ * clamped, or decreasing, where nothing counts: counts, tokens and loss are 0). */
 size_t strata_moe_balance_workspace(const strata_moe *h, int n_tokens, int n_seq);
 strata_status strata_moe_balance(strata_moe *h, const float *logits, const int32_t *idx,
                                  int n_tokens, const int32_t *seq_off, int n_seq,

@@ -309,6 +309,16 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceP
     __syncthreads();
     t = e;
   }
+  // Offsets that decrease have no such pieces, and the slots that the next kernel
+  // would read were not all written: it is told to count nothing.  (By the last
+  // block, whose chunk is the shortest.)
+  if (p.seq_off && blockIdx.x == gridDim.x - 1) {
+    int falls = 0;
+#pragma unroll 4
+    for (int b = tid; b < p.n_seq; b += kSumThreads) falls |= p.seq_off[b] > p.seq_off[b + 1];
+    falls = __syncthreads_or(falls);
+    if (tid == 0) *p.falls = falls;
+  }
 }
 
 // Adds the slots of each sequence's pieces.  A cluster takes up to 4 sequences
@@ -345,7 +355,8 @@ __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(const Ba
     if (p.seq_off && share == 0 && lane == 0 && (p.seq_off[b] != sp.a || p.seq_off[b + 1] != sp.e))
       set_status(p.status, STATUS_BOUNDS);
     const int c0 = sp.a / p.chunk;
-    const int n = sp.e > sp.a ? (sp.e - 1) / p.chunk - c0 + 1 : 0;
+    const bool none = sp.e <= sp.a || (p.seq_off && *p.falls != 0);
+    const int n = none ? 0 : (sp.e - 1) / p.chunk - c0 + 1;
     // (at most 148 slots: five loads a lane; they are waited for at the end)
     int t[5];
 #pragma unroll
@@ -582,7 +593,7 @@ inline bool vec_rows(const void *p, int E) {
 
 size_t balance_workspace(int T, int E, int n_seq) {
   const size_t slots = (size_t)sum_blocks(T) + n_seq;
-  return 2 * up256(slots * E * 4) + up256(slots * 4) + up256((size_t)n_seq * 8);
+  return 2 * up256(slots * E * 4) + up256(slots * 4) + up256((size_t)n_seq * 8) + up256(4);
 }
 
 cudaError_t run_balance(BalanceParams p, void *workspace, cudaStream_t stream) {
@@ -592,6 +603,7 @@ cudaError_t run_balance(BalanceParams p, void *workspace, cudaStream_t stream) {
   p.part_cnt = reinterpret_cast<int *>(w += up256(slots * p.E * 4));
   p.part_tok = reinterpret_cast<int *>(w += up256(slots * p.E * 4));
   p.seq_loss = reinterpret_cast<double *>(w += up256(slots * 4));
+  p.falls = reinterpret_cast<int *>(w += up256((size_t)p.n_seq * 8));
   p.chunk = sum_chunk(p.T);
   const bool whole = whole_batch(p);
   cudaError_t e =

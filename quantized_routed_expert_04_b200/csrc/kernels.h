@@ -132,6 +132,7 @@ struct BalanceParams {
   float *part_p;           // [blocks + n_seq][E] sums of p per piece
   int *part_cnt, *part_tok;
   double *seq_loss;        // [n_seq]
+  int *falls;              // [1] whether seq_off decreases
 };
 struct BalanceGradParams {
   BalanceParams p;         // counts and tokens are inputs; no idx, loss

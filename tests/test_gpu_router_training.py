@@ -780,3 +780,49 @@ def test_route_backward_tokens_in_a_row_select_the_same_experts(T, E, k, want):
         check_route_backward(layer, x, None, logits, idx, dw, None, "softmax", want=want)
         idx = (E - 1 - idx).contiguous()
     layer.close()
+
+
+# Decreasing offsets: nothing counts, whatever an earlier call left in the workspace
+@pytest.mark.parametrize("T,off", [(100, [0, 50, 40, 100]), (100, [0, 1 << 30, 3]), (700, [0, 300, 290, 310, 700]),
+                                   (700, [0, 200, 320, 100, 150, 700]), (5000, [4000, 3000, 5000]),
+                                   (300, [300, 0]), (9000, list(range(2000, 0, -1)) + [9000])])
+def test_balance_decreasing_offsets_count_nothing(T, off):
+    E, k = 64, 4
+    layer = make_layer(E, k)
+    logits, idx = routing(T, E, k, 191)
+    n = len(off) - 1
+    seq = torch.tensor(off, dtype=torch.int32, device="cuda")
+    ws = torch.empty(layer.balance_workspace(T, n), dtype=torch.uint8, device="cuda")
+    ordered = torch.tensor(sorted(min(o, T) for o in off), dtype=torch.int32, device="cuda")
+    for before in (None, ordered):
+        counts = torch.full((n, E), -7, dtype=torch.int32, device="cuda")
+        tokens, loss = torch.full((n,), -7, dtype=torch.int32, device="cuda"), torch.full((1,), 7.0, device="cuda")
+        d = torch.full((T, E), 7.0, device="cuda")
+        if before is None:
+            ws.fill_(0xFF)
+        else:
+            layer.balance(logits, idx, 0.5, counts, tokens, loss, ws, before)
+            assert int(layer.status()[0]) == 0
+        layer.balance(logits, idx, 0.5, counts, tokens, loss, ws, seq)
+        st, bits = layer.status()
+        assert st == binding.Status.DEVICE_STATUS and bits == 8
+        layer.balance_backward(logits, 0.5, counts, tokens, d, None, seq)
+        assert float(loss) == 0 and not counts.any() and not tokens.any() and not d.any()
+    layer.close()
+
+
+# Offsets that only leave the tokens are clamped
+def test_balance_offsets_outside_are_clamped():
+    T, E, k = 700, 64, 4
+    layer = make_layer(E, k)
+    logits, idx = routing(T, E, k, 192)
+    for off, inside in (([-9, 100, 400, 700], [0, 100, 400, 700]), ([0, 333, 1 << 30], [0, 333, 700]),
+                        ([-5, -2, 20, 800, 900], [0, 0, 20, 700, 700])):
+        want = run_balance(layer, logits, idx, 0.5, off=inside)
+        assert int(layer.status()[0]) == 0
+        got = run_balance(layer, logits, idx, 0.5, off=off)
+        st, bits = layer.status()
+        assert st == binding.Status.DEVICE_STATUS and bits == 8
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+    layer.close()
