@@ -390,8 +390,9 @@ struct NormGradParams {
 // through the ring with elements converted one by one), now 44 us.  The barrier
 // of the row's reduction also frees its stage: every thread has its elements in
 // registers by then.  A copy that does not arrive within the limit of its wait
-// ends the copies; its row and all the thread's rows behind it become NaN, and
-// with them the weight's gradient.  Without kVec (rows that 16-byte copies cannot walk) the
+// ends the copies, after those in flight have had as long again each to land; its
+// row and all the thread's rows behind it become NaN, and with them the weight's
+// gradient.  Without kVec (rows that 16-byte copies cannot walk) the
 // next row's elements are loaded into registers ahead.
 template <typename T, int kTpr, int kRows, int kNe, bool kVec, int kMinBlocks>
 __global__ void __launch_bounds__(kTpr *kRows, kMinBlocks) norm_grad_kernel(const NormGradParams p) {
@@ -496,7 +497,15 @@ __global__ void __launch_bounds__(kTpr *kRows, kMinBlocks) norm_grad_kernel(cons
       }
     };
     if (kVec) {
-      lost = lost || !mbar_wait(&full[st], phase, nullptr);
+      if (!lost && !mbar_wait(&full[st], phase, nullptr)) {
+        lost = true;
+        // (the ring's memory is used again below, and the block's after its end)
+        if (tid == 0)
+          for (int k = 0; k < p.stages && row + k * step < p.T; ++k) {
+            const int s = st + k < p.stages ? st + k : st + k - p.stages;
+            (void)mbar_wait(&full[s], s >= st ? phase : phase ^ 1u, nullptr);
+          }
+      }
 #pragma unroll
       for (int i = 0; i < kNe; i += 8) {
         unpack_at(i, a + (kHold ? i : 0), d + (kHold ? i : 0));
