@@ -798,6 +798,7 @@ strata_status strata_rmsnorm(int dtype, const void *x, long long x_stride, const
     return STRATA_ERR_INVALID_ARG;
   if (hidden > kNormMaxH) return STRATA_ERR_UNSUPPORTED;
   if (residual_out && residual_out == out) return STRATA_ERR_INVALID_ARG;
+  if (n_tokens == 1) x_stride = residual_stride = residual_out_stride = out_stride = hidden;
   if (out_q8 ? !scales || (group != 32 && group != 64 && group != 128 && group < hidden)
              : scales != nullptr)
     return STRATA_ERR_INVALID_ARG;
@@ -870,6 +871,7 @@ strata_status strata_rmsnorm_backward(int dtype, const void *h, long long h_stri
     return STRATA_ERR_INVALID_ARG;
   if (hidden > kNormMaxH) return STRATA_ERR_UNSUPPORTED;
   if (!aligned(dweight, 4)) return STRATA_ERR_INVALID_ARG;
+  if (n_tokens == 1) h_stride = dout_stride = dsum_stride = dx_stride = hidden;
   if (n_tokens == 0)
     return dweight ? status_of(cudaMemsetAsync(dweight, 0, sizeof(float) * hidden, stream)) : STRATA_OK;
   if (!rows_ok(h, h_stride, n_tokens, hidden, b) || !weight || !aligned(weight, 4) ||

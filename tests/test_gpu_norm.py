@@ -297,3 +297,26 @@ def test_streams_and_graphs():
             assert torch.equal(ro, b["ro"]) and torch.equal(out, b["out"])
             assert torch.equal(dx, b["dx"]) and torch.equal(dw, b["dw"])
     assert bwant[0].shape == (T, H)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_one_row_is_the_same_in_any_stride(dt):
+    H = 4096
+    w = weight(H)
+
+    def row(seed, ld):
+        return rows(1, H, dt, seed).as_strided((1, H), (ld, 1))
+
+    got = []
+    for ld in (H, H + 1, 3):
+        x, r, dy, ds = (row(s, ld) for s in (1, 2, 3, 4))
+        ro, out = (torch.empty(1, H, dtype=DT[dt], device="cuda").as_strided((1, H), (ld, 1)) for _ in range(2))
+        binding.strata_rmsnorm(x, r, w, EPS, ro, out)
+        dx, dg = torch.empty(1, H, dtype=DT[dt], device="cuda"), torch.empty(H, device="cuda")
+        ws = torch.empty(binding.strata_rmsnorm_backward_workspace(1, H), dtype=torch.uint8, device="cuda")
+        binding.strata_rmsnorm_backward(ro, w, EPS, dy, ds, dx, dg, ws)
+        got.append((ro, out, dx, dg))
+    for a, b in zip(got[0], got[1]):
+        assert torch.equal(a, b)
+    for a, b in zip(got[0], got[2]):
+        assert torch.equal(a, b)
