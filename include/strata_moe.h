@@ -531,7 +531,9 @@ strata_status strata_moe_balance_backward(strata_moe *h, const float *logits, in
  * sums in a fixed order); for dx, which is rounded to bf16, dl and W are taken to
  * 22 bits (two f16 numbers, each token's dl and each 32 columns of W times a power
  * of two first, so whatever their size).  A dl
- * that is not finite, or of magnitude above 3.3e38, gives NaN.  n_tokens == 0
+ * that is not finite makes dW and db of its expert and dx of its token infinite
+ * or NaN, all of them and no others; one of magnitude above 3.38e38 may do so in
+ * dW.  n_tokens == 0
  * zeroes dW and db.
  * dx must not share memory with x.
  * Host errors: INVALID_ARG, CUDA.  Device errors: DEVICE_STATUS (bit 2: an id

@@ -826,3 +826,24 @@ def test_balance_offsets_outside_are_clamped():
         for a, b in zip(want, got):
             assert torch.equal(a, b)
     layer.close()
+
+
+# A gradient that is not finite shows wherever it reaches, and nowhere else: zeros in
+# x and W do not hide it
+@pytest.mark.parametrize("T,E", [(20, 64), (300, 40), (300, 100), (700, 256)])   # one launch, three
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+def test_route_backward_of_a_gradient_that_is_not_finite(T, E, value):
+    H, t, e = 256, 17, 5
+    W, x = router(E, H, 201), acts(T, H, 202)
+    W[:, ::3] = 0
+    x[:, ::3] = 0
+    layer = make_layer(E, 2, H=H, W=W)
+    d = torch.randn(T, E, device="cuda", generator=gen(203))
+    d[t, e] = value
+    out = run_route_backward(layer, x, None, None, None, d)
+    assert int(layer.status()[0]) == 0
+    lost = {n: ~v.isfinite() for n, v in out.items()}
+    assert bool(lost["dx"][t].all()) and int(lost["dx"].sum()) == H
+    assert bool(lost["dW"][e].all()) and int(lost["dW"].sum()) == H
+    assert bool(lost["db"][e]) and int(lost["db"].sum()) == 1
+    layer.close()
