@@ -602,7 +602,7 @@ class StrataMoE:
         sa, ma = _flat(seq_off, dev, n_seq * 4 + 4, _I32, w), _flat(mask, dev, T, _BYTES, w)
         loa = _flat(loss, dev, 4, _F32, w)
         ws, nws = _workspace(workspace, dev, w)
-        _packed_balance(w, self.h, la, ia, T, sa, n_seq, ma, coef, ca, ta, loa, ws, nws,
+        _packed_balance(w, self.h or 0, la, ia, T, sa, n_seq, ma, coef, ca, ta, loa, ws, nws,
                         _stream_on(stream, dev, w))
 
     def balance_backward(self, logits, coef, counts, tokens, dlogits, dloss=None, seq_off=None,
@@ -614,7 +614,7 @@ class StrataMoE:
         ca, ta = _flat(counts, dev, n_seq * E * 4, _I32, w), _flat(tokens, dev, n_seq * 4, _I32, w)
         sa, ma = _flat(seq_off, dev, n_seq * 4 + 4, _I32, w), _flat(mask, dev, T, _BYTES, w)
         dla = _flat(dloss, dev, 4, _F32, w)
-        _packed_balance_backward(w, self.h, la, T, sa, n_seq, ma, coef, ca, ta, dla, da,
+        _packed_balance_backward(w, self.h or 0, la, T, sa, n_seq, ma, coef, ca, ta, dla, da,
                                  _stream_on(stream, dev, w))
 
     def route_backward_workspace(self, n_tokens):
@@ -629,7 +629,7 @@ class StrataMoE:
         ia, dwa = _flat(idx, dev, T * k * 4, _I32, w), _flat(dw, dev, T * k * 4, _F32, w)
         dWa, dba = _flat(dW, dev, E * H * 4, _F32, w), _flat(db, dev, E * 4, _F32, w)
         ws, nws = _workspace(workspace, dev, w)
-        _packed_route_backward(w, self.h, xa, T, la, ia, dwa, dla, dWa, dba, dxa, ws, nws,
+        _packed_route_backward(w, self.h or 0, xa, T, la, ia, dwa, dla, dWa, dba, dxa, ws, nws,
                                _stream_on(stream, dev, w))
 
     def status(self, stream=None):

@@ -131,3 +131,23 @@ def test_operands_of_more_than_one_type(reached):
         norm(**a)
         norm_backward(**{n: v.to(dt) if v.dtype is BF16 else v for n, v in CALLS[norm_backward]().items()})
     assert len(reached) == 8
+
+
+def test_a_closed_layer_is_refused():
+    # (a null handle goes to the library, which refuses it before anything else)
+    from quantized_routed_expert_04_b200 import build
+    build.build()
+    closed = Layer()
+    closed.h = None
+    a, b, r = CALLS[balance](), CALLS[balance_backward](), CALLS[route_backward]()
+    with pytest.MonkeyPatch.context() as m:
+        m.setattr(binding, "_stream_on", lambda stream, dev, where: 0)
+        for call in (lambda: closed.balance(a["logits"], a["idx"], 0.1, a["counts"], a["tokens"], a["loss"],
+                                            a["workspace"], a["seq_off"], a["mask"]),
+                     lambda: closed.balance_backward(b["logits"], 0.1, b["counts"], b["tokens"], b["dlogits"],
+                                                     b["dloss"], b["seq_off"], b["mask"]),
+                     lambda: closed.route_backward(*(r[n] for n in ("x", "logits", "idx", "dw", "dlogits", "dW",
+                                                                    "db", "dx", "workspace")))):
+            with pytest.raises(binding.StrataError) as e:
+                call()
+            assert e.value.status == binding.Status.INVALID_ARG
