@@ -296,7 +296,7 @@ def _of_kind(t, kind):
         torch = _get_torch()
         _BF16.append(torch.bfloat16)
         _I32.append(torch.int32)
-        _BYTES.extend((torch.uint8, torch.bool))
+        _BYTES.extend((torch.uint8, torch.bool, torch.int8))
         _E4M3.extend((torch.float8_e4m3fn, torch.uint8))
         _F32.append(torch.float32)
     return t.dtype in kind

@@ -124,13 +124,13 @@ def test_operands(call, reached):
 
 def test_operands_of_more_than_one_type(reached):
     for call, name, good in ((norm, "out_q8", t(U8, T, H)), (forward_q8, "x_q8", t(U8, T, H)),
-                             (balance, "mask", t(torch.bool, T)), (balance_backward, "mask", t(torch.bool, T))):
+                             (balance, "mask", t(torch.bool, T)), (balance, "mask", t(torch.int8, T)), (balance_backward, "mask", t(torch.bool, T))):
         call(**{**CALLS[call](), name: good})
     for dt in (F16, F32):
         a = {n: v.to(dt) if v.dtype is BF16 else v for n, v in CALLS[norm]().items()}
         norm(**a)
         norm_backward(**{n: v.to(dt) if v.dtype is BF16 else v for n, v in CALLS[norm_backward]().items()})
-    assert len(reached) == 8
+    assert len(reached) == 9
 
 
 def test_a_closed_layer_is_refused():
