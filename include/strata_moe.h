@@ -397,8 +397,10 @@ enum { STRATA_DTYPE_BF16 = 0, STRATA_DTYPE_F16 = 1, STRATA_DTYPE_F32 = 2 };
  * scale per `group` consecutive columns of a row, scales [n_tokens]
  * [ceil(hidden / group)]: scale = max(largest |y| of the group / 448, 2^-126),
  * q = e4m3(y * (1 / scale)) (1 / scale and the product in fp32, then nearest
- * even); y is the fp32 value, not the rounded out.  group: 32, 64, 128, or >= hidden for one scale a row.  A group that
- * holds a NaN gets a NaN scale.
+ * even); y is the fp32 value, not the rounded out.  group: 32, 64, 128, or
+ * >= hidden for one scale a row.  A group that holds a NaN gets a NaN scale.
+ * The sum of squares is taken in fp32 as it is: a row whose squares leave fp32's
+ * range (elements above about 1e17, or below 1e-22 with eps 0) is not normalised.
  * 16-byte aligned rows of a multiple of 8 elements are fastest; any element
  * alignment works.  Runs on the current device, asynchronous on `stream`; no
  * workspace.  Errors: INVALID_ARG, UNSUPPORTED (hidden > 16384), CUDA. */
@@ -442,20 +444,24 @@ strata_status strata_moe_forward_norm(strata_moe *h, const void *x_bf16, const v
                                       void *residual_out_bf16, void *normed_bf16, void *out_bf16,
                                       strata_stream_t stream);
 
-/* The layer on activations in 8 bits, as strata_rmsnorm writes them (half the
- * bytes of bf16 where rows travel between the norm and the layer): x_q8 device
- * e4m3 [n_tokens][hidden], 16-byte aligned, scales device fp32 [n_tokens]
+/* The layer on activations in 8 bits, as strata_rmsnorm writes them, for rows that
+ * were kept or sent in that form (half the bytes of bf16; the call itself expands
+ * them in device memory first and is no faster than strata_moe_forward): x_q8
+ * device e4m3 [n_tokens][hidden], 16-byte aligned, scales device fp32 [n_tokens]
  * [ceil(hidden / group)], group 32, 64, 128 or >= hidden.  x_bf16 (device bf16
  * [n_tokens][hidden], 16-byte aligned, sharing no memory with x_q8 or out)
- * receives q * scale, rounded once, and the result is strata_moe_forward's of it.  Runs on the handle's device, which
- * must be the current one.  Errors: as strata_moe_forward. */
+ * receives q * scale, rounded once, and the result is strata_moe_forward's of it.
+ * Runs on the handle's device, which must be the current one.  Errors: as strata_moe_forward. */
 strata_status strata_moe_forward_q8(strata_moe *h, const void *x_q8, const float *scales, int group,
                                     int n_tokens, void *x_bf16, void *out_bf16,
                                     strata_stream_t stream);
 
 /* ---- Training the router over frozen experts.  The pages describe no
  * training; these calls go with strata_moe_route, whose logits and idx they
- * take.  They keep nothing in the handle but the device status word, run on the
+ * take.  The gradient that reaches the routing weights w from the layer's output
+ * (dw[t][j] = dout[t] . the output of expert idx[t][j], unweighted) is the
+ * caller's to bring: no call here gives the experts' single outputs.  Without it
+ * the balance loss alone moves the router.  They keep nothing in the handle but the device status word, run on the
  * handle's device (which must be the current one) and use the caller's
  * workspace: device memory, 16-byte aligned, of at least the size that the
  * *_workspace call gives for the same arguments, written before it is read.

@@ -18,8 +18,11 @@ inline strata_status status_of(cudaError_t e) {
 }
 
 // Launch with programmatic dependent launch: the grid may be set up while the
-// kernel before it on the stream drains (every kernel launched this way
-// begins with griddepcontrol.wait, before any access to global memory).
+// kernel before it on the stream drains.  Every kernel launched this way begins
+// with griddepcontrol.wait, before any access to global memory, and lets the next
+// one start only after that: so a grid that starts finds all work before its
+// predecessor complete.  One relies on that alone: route_grad_dx_kernel reads what
+// the grid before its predecessor wrote without a wait of its own.
 template <typename... Exp, typename... Act>
 cudaError_t launch_pdl(void (*kern)(Exp...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t stream, Act &&...args) {

@@ -354,7 +354,8 @@ __global__ void __launch_bounds__(kTpr *kRows) norm_kernel(const NormParams p) {
 // Threads per row: 16 elements each at the widths where a row has the threads to
 // itself (8192 x 4096 bf16 with residual and 8-bit output: 49.5 us with 256
 // threads, 50.3 with 128 of 32 elements, 51.8 with 512 of 8), fewer on short
-// rows, where a warp has one.
+// rows, where a warp has one.  Rows that 16-byte accesses cannot walk go element by
+// element: 8192 x 4095 91 us; 2048 x 16383 123 us, 67 with 16384.
 template <typename T, bool kVec>
 cudaError_t launch_norm(const NormParams &p, cudaStream_t stream) {
   const int H = p.H, T_ = p.T;
@@ -393,7 +394,10 @@ struct NormGradParams {
 // ends the copies, after those in flight have had as long again each to land; its
 // row and all the thread's rows behind it become NaN, and with them the weight's
 // gradient.  Without kVec (rows that 16-byte copies cannot walk) the
-// next row's elements are loaded into registers ahead.
+// next row's elements are loaded into registers ahead, 2 or 4 bytes an access: 8192
+// rows of 4095 bf16 78 us, 50 with 4096; and above 8192 columns a thread's 64
+// registers do not hold both rows (556 to 668 bytes a thread are spilled: 2048 rows
+// of 16383 bf16 220 us, 75 with 16384).
 template <typename T, int kTpr, int kRows, int kNe, bool kVec, int kMinBlocks>
 __global__ void __launch_bounds__(kTpr *kRows, kMinBlocks) norm_grad_kernel(const NormGradParams p) {
   constexpr int kWarps = kTpr / 32;

@@ -10,8 +10,8 @@
 //
 // Three launches: the operands in 16 bits; dW on the tensor cores (tcgen05,
 // accumulators in tensor memory); dx on the tensor cores, whose spare warps, and
-// after dx the others, add up the parts of dW and db.  A few tokens take one launch on the fp32 units
-// instead (few_tokens below).
+// after dx the others, add up the parts of dW and db.  A few tokens take one launch
+// on the fp32 units instead (few_tokens below).
 //
 // 8192 tokens x 256 experts x 4096: 89 us replayed, 106 with fresh inputs (alone
 // and with caches flushed the preparation takes 13, dW 45, dx 44).  Both products
@@ -824,10 +824,15 @@ __global__ void __launch_bounds__(kDxThreads, 1)
   pair_begin(s, p.stages, kDxEpiWarps, warp);
   const uint32_t tmem = s.tmem, rank = cluster_rank();
   // dx needs what the preparation wrote, and the dW kernel lets this grid start
-  // only once all its blocks have seen the preparation complete: only the warps
-  // that add up dW's parts wait for the dW kernel itself, so that dx runs beside
-  // it wherever multiprocessors are free (128 tokens x 64 experts x 2048: 10.5 us,
-  // 13.4 with every warp waiting; 8192 x 256 x 4096: 70.9 and 71.7).
+  // only once all its blocks have waited for the preparation, whose writes are then
+  // in L2: only the warps that add up dW's parts wait for the dW kernel itself, so
+  // that dx runs beside it wherever multiprocessors are free (128 tokens x 64
+  // experts x 2048: 10.5 us, 13.4 with every warp waiting; both with dx in one
+  // product).  The programming model promises those writes only to a thread that
+  // waits itself; here they are read by bulk tensor loads and __ldcg, which go to
+  // L2, never through an L1 that could hold older lines.  What this needs: every
+  // block of dW waits before it lets this grid start, the warps above read nothing
+  // that dW's kernel writes, and dx shares no memory with x (the host refuses it).
   if (!p.after_dw || warp >= 2 + kDxEpiWarps) {
     grid_dependency_wait();
     grid_dependency_launch();
