@@ -173,9 +173,11 @@ constexpr float kWLimit = kF16Overflow / 256.0f;
 // Blocks 0 .. tok_blocks - 1: rows of dl, a group of kG lanes per token, each lane
 // 8 consecutive experts, as three bf16 pieces and as two of scaled f16, and the
 // block's share of db.  The blocks behind them: 32 columns of W likewise, all experts
-// in registers between the search for the largest and the rounding.  (kG holds the experts and the
-// selections; a warp per token whatever their number made the whole call over
-// 8192 tokens x 32 experts x 4096 take 44.1 us, 42.2 with 8 lanes each.)
+// in registers between the search for the largest and the rounding.  (kG holds the
+// experts and the selections; a warp per token whatever their number made the whole
+// call over 8192 tokens x 32 experts x 4096 take 44.1 us, 42.2 with 8 lanes each, both
+// with dx in one product.  Two blocks a multiprocessor: with 72 registers a thread
+// and one, 8192 tokens x 256 experts took 4 us more.)
 template <int kG>
 __global__ void __launch_bounds__(32 * kPrepWarps, 2) route_grad_prep_kernel(const RouteGradParams p) {
   constexpr int kTok = 32 / kG;   // tokens a warp works on at once
@@ -515,7 +517,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int la
 //   form 2, up to 256 experts:  three: hi, mid, lo, 256 columns each
 // and the epilogue adds the columns of an expert.  Whole calls over 4096 h, in
 // form 2 and in their own: 32 experts x 2048 tokens 26.5 and 19.9 us, 128 experts
-// 29.0 and 23.2, 64 experts x 8192 tokens 59.4 and 43.2.
+// 29.0 and 23.2, 64 experts x 8192 tokens 59.4 and 43.2 (with dx in one product).
 //
 // A stage is 32 tokens in form 2 (7 stages of 32 KB) and 64 in the others, whose
 // MMAs take less time than issuing the copies of so small boxes: a pair with a
@@ -1215,10 +1217,10 @@ int h_tiles(int H) { return (H + kTileH - 1) / kTileH; }
 // written and read again, only then can dW be added up, and pairs that dW leaves
 // free have dx to do.  The costs below, in us, follow measurements of whole calls
 // at 256 to 7168 h, 32 to 256 experts, 64 to 8192 tokens.  E.g. 4096 h x 256
-// experts: 256 tokens 17.0 us with m = 1, 24.1 with 4, 24.9 with 74 runs; 1024
-// tokens 32.5, 26.3 (m = 3, which is taken: 26.0) and 28.2; 8192 tokens 147, 71.4
-// and 72.4.  1024 h x 32 experts: 1024 tokens 11.3 with m = 8, 14.1 with 18; 8192
-// tokens 21.1 and 19.8.  7168 h x 256 experts: 8192 tokens 114.6 with m = 2, 112.2
+// experts: 256 tokens 17.7 us with m = 1, 27.0 with 4, 27.9 with 74 runs; 1024
+// tokens 35.6, 29.6 (29.2 with 3, which is taken) and 30.8; 8192 tokens 163, 87.6
+// and 85.8.  1024 h x 32 experts: 1024 tokens 11.6 with m = 8, 13.4 with 18; 8192
+// tokens 21.4 and 20.0.  7168 h x 256 experts: 8192 tokens 141 with m = 2, 137
 // with 74 runs.
 int dw_pairs(int T, int E, int H) {
   const int tiles = h_tiles(H);
@@ -1293,11 +1295,12 @@ size_t route_grad_workspace(int T, int E, int H) { return layout(T > 0 ? T : 1, 
 // us, that follow measurements of both forms from 8 to 256 experts and 256 to
 // 16384 h: a block's products, its rows of dl, and as many rounds of blocks as
 // there are; the other form's launches, and its preparation of more experts.  E.g.
-// 2048 h: 8 experts 9.5 against 11.1 us with 320 tokens, 14.3 against 12.9 with
-// 640; 64 experts 8.6 against 10.3 with 80, 13.4 against 10.6 with 160; 128
-// experts 10.3 against 11.6 with 60, 18.7 against 12.4 with 140; 7168 h x 64
-// experts 8.8 against 9.8 with 10, 13.1 against 10.2 with 40.  (At most 76 KB of
-// dl and W, 24 of x and 16 of parts in shared memory.)
+// 2048 h: 8 experts 9.5 against 10.8 us with 320 tokens, 14.2 against 11.8 with
+// 640; 64 experts 8.5 against 11.0 with 80, 13.3 against 11.3 with 160; 128
+// experts 10.1 against 11.8 with 60, 18.5 against 12.4 with 140; 7168 h x 64
+// experts 8.8 against 10.1 with 10, 12.9 against 10.7 with 40.  In between it is up
+// to 1.5 us off (2048 h x 64 experts x 110 tokens: 9.8 against 11.3, taken).  (At
+// most 78 KB of shared memory.)
 bool few_tokens(int T, int E, int H) {
   const int hs = small_hs(H);
   const double rounds = std::max(1.0, H / hs / 148.0);
@@ -1367,15 +1370,15 @@ cudaError_t run_route_grad(RouteGradParams p, void *workspace, cudaStream_t stre
     const int smem = fixed + d.stages * kDxStage + 1024;
     // (pairs without an item of dx help with the sums, a row of 256 or an expert
     // per warp; not many more than dW leaves room for, since those start late: 1024
-    // tokens x 256 h x 256 experts 19.7 us with 64 pairs, 16.7 with 37)
+    // tokens x 256 h x 256 experts 18.5 us with 64 pairs, 18.2 with 37)
     const int sums = sum_rows(q);
     const int help = std::min((sums + 2 * kSumWarps - 1) / (2 * kSumWarps), std::max(kPairs - pairs, kPairs / 2));
     const int grid = std::min(std::max(items, help), kPairs);
     d.per = items / grid;
     d.extra = items % grid;
-    // a row takes a spare warp about 1.2 us and an item of dx its pair 2.5: what the
+    // a row takes a spare warp about 1.2 us and an item of dx its pair 2.3 to 3.6: what the
     // spare warps would not have done by the end of dx, the epilogue's do then (2048
-    // tokens x 1024 h x 256 experts: 20.0 us, 22.6 with the spare warps alone)
+    // tokens x 1024 h x 256 experts: 21.3 us, 24.7 with the spare warps alone)
     d.spare_rows = (int)std::min<long long>(sums, 2LL * grid * kSumWarps * (1 + 2 * (items / grid)));
     e = cudaFuncSetAttribute(route_grad_dx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
     if (e == cudaSuccess)
